@@ -125,7 +125,7 @@ def _quantise(X, fmt):
     if fmt == NVFP4:
         bits = x.abs().amax(1).view(torch.int32)
         f = (bits >> 23) - 11 + ((bits & 0x7FFFFF) > 0x280000).to(torch.int32)
-        f = torch.where(bits == 0, torch.full_like(f, 127), f.clamp(min=1))
+        f = torch.where(bits == 0, torch.full_like(f, 127), f.clamp(min=27))      # at least 2^-100
         s = _pow2(f)
         x = x * _pow2(254 - f)[:, None]
         amax = x.abs().view(rows, K // b, b).amax(2)
@@ -371,7 +371,7 @@ def _exact_quantised(X, fmt):
         top = x.abs().amax(1) / 2688
         one = torch.ones_like(top)
         mant, e = torch.frexp(top)                     # top = mant 2^e, mant in [0.5, 1)
-        s = torch.ldexp(one, torch.where(mant == 0.5, e - 1, e).clamp(min=-126))
+        s = torch.ldexp(one, torch.where(mant == 0.5, e - 1, e).clamp(min=-100))
         s = torch.where(top == 0, one, s)
         y = (x / s[:, None]).view(rows, -1, 16)
         S = _exact_grid(y.abs().amax(2) / 6, -6, 3, 448.0)[:, :, None]
