@@ -88,7 +88,9 @@ typedef enum {
   QLORA_OP_FWD = 1,
   QLORA_OP_BWD = 2,
   QLORA_OP_FWD_DROPOUT = 3,
-  QLORA_OP_BWD_DROPOUT = 4
+  QLORA_OP_BWD_DROPOUT = 4,
+  QLORA_OP_MX_FWD = 5,        /* qlora_mx_linear_fwd, either format, r may be 0 */
+  QLORA_OP_MX_BWD = 6         /* qlora_mx_linear_bwd, likewise                  */
 } qlora_op;
 
 /* LoRA dropout on the adapter's input ([QE] config walk-through:
@@ -144,7 +146,47 @@ typedef struct {
   int32_t quant_type;     /* QLORA_QUANT_NF4 or QLORA_QUANT_FP4 */
 } nf4_weight;
 
+/* Microscaled 4-bit formats: E2M1 elements (magnitudes 0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6; code = float bits) under a block scale that the tensor cores apply.
+ *   QLORA_MXFP4: blocks of 32 consecutive elements of a row, scale byte
+ *     e + 127 (E8M0) for 2^e, e = max(floor(log2 amax) - 2, -127).
+ *   QLORA_NVFP4: blocks of 16, scale byte E4M3, and an fp32 scale s per row,
+ *     the smallest power of two >= 2^-100 with amax_row <= 6 * 448 * s (1 for
+ *     a zero row); block scale S = E4M3(amax / s / 6).
+ * Roundings are to nearest, ties to even, magnitudes above 6 become 6; a value
+ * that rounds to zero may be stored as code 8 (-0). */
+typedef enum { QLORA_MXFP4 = 0, QLORA_NVFP4 = 1 } qlora_mx_format;
+
+/*
+ * A microscaled matrix [rows, cols], a weight or quantised activations.
+ *   packed    [rows * cols / 2]  two codes per byte, element 2j in the LOW
+ *             nibble (the tensor cores' order; nf4_weight has it high)
+ *   scales    [qlora_mx_scale_bytes(format, rows, cols)] scale bytes in tiles
+ *             of 128 rows x 4 scale columns: scale (r, c) is byte
+ *             ((r / 128) * ceil(C / 4) + c / 4) * 512 + (r % 32) * 16 +
+ *             (r % 128 / 32) * 4 + c % 4, C = cols / block; bytes of rows and
+ *             columns past the matrix are 0
+ *   row_scale [rows] fp32 (NVFP4; unused for MXFP4).  The quantiser writes
+ *             powers of two; any finite positive values are accepted (one
+ *             scale for the whole tensor is that scale repeated)
+ * Value of an element: e2m1(code) * scale (MXFP4), RN32(e2m1(code) * S * s)
+ * (NVFP4).  cols % 32 == 0.
+ */
+typedef struct {
+  const uint8_t* packed;
+  int64_t rows;
+  int64_t cols;
+  int32_t format;         /* QLORA_MXFP4 or QLORA_NVFP4 */
+  int32_t reserved;       /* 0 */
+  const uint8_t* scales;
+  const float* row_scale;
+} qlora_mx_tensor;
+
 /* ---- host-only queries (no GPU needed) -------------------------------- */
+
+/* Bytes of the scale array of a microscaled [rows, cols] matrix (0 for a bad
+ * format or shape). */
+size_t qlora_mx_scale_bytes(int format, int64_t rows, int64_t cols);
 
 /* The library's 16-entry NF4 table and its 15 decision thresholds, computed
  * on the host at load time ([QE] "Put the rows where the weights are",
@@ -171,7 +213,8 @@ int qlora_dq_mean_from_hist(const int64_t* hist, int64_t n_total, float* mean);
 
 /* Bytes of caller workspace needed by an operation (0 if none).
  *   QLORA_OP_DOUBLE_QUANT: M, K, r ignored; N = number of absmax values.
- *   QLORA_OP_FWD / QLORA_OP_BWD: layer with M tokens, weight N x K, rank r. */
+ *   QLORA_OP_FWD / QLORA_OP_BWD: layer with M tokens, weight N x K, rank r.
+ *   QLORA_OP_MX_FWD / QLORA_OP_MX_BWD: the same, r = 0 for no adapter. */
 size_t qlora_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r);
 
 /* Human-readable name of a status code (static string). */
@@ -346,6 +389,82 @@ int qlora_linear_bwd_dropout(const nf4_weight* w, const void* X, const void* dY,
                              float alpha, const qlora_dropout* dropout, const void* T,
                              void* dX, void* dA, void* dB, void* ws, size_t ws_bytes,
                              qlora_stream_t stream);
+
+/*
+ * Microscaled 4-bit quantisation of a matrix whose rows are `ld` elements
+ * apart (see qlora_mx_format).  Serves weights and activations: a row's codes
+ * and scales depend on that row alone.
+ *   X         device [rows, cols], fp32 or bf16, ld >= cols
+ *   packed, scales, row_scale  device out (see qlora_mx_tensor); row_scale may
+ *             be NULL for MXFP4.  Padding bytes of `scales` are written as 0.
+ * A block that holds a NaN or an infinity gets the format's NaN scale (0xFF,
+ * or 0x7F) and zero codes, so it dequantises to NaN and makes the products
+ * that read it NaN; it does not enter the row's maximum, and
+ * QLORA_ERR_NONFINITE is set in the device status word.
+ * Constraints: rows >= 1, cols >= 32, cols % 32 == 0, rows of X 16-byte aligned.
+ */
+int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
+                      uint8_t* packed, uint8_t* scales, float* row_scale, qlora_stream_t stream);
+
+/* out [rows, cols] bf16 = RNbf16 of the elements' values; exact for row scales
+ * that are powers of two, results below bf16's range apart. */
+int qlora_mx_dequantize(const qlora_mx_tensor* t, void* out, qlora_stream_t stream);
+
+/*
+ * Product of two microscaled matrices of one format:
+ *   Y[M, N] = RNbf16( deq(x) deq(w)^T ),  x [M, K], w [N, K]
+ * on the block-scaled tensor cores (the scales are applied inside the product,
+ * sums in fp32), any M, N >= 1, no workspace.  A row's result does not depend
+ * on the other rows of x.  The order of the sum depends on the shapes alone.
+ */
+int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y, qlora_stream_t stream);
+
+/*
+ * The QLoRA layer on a frozen microscaled base.  X is quantised to w's format
+ * inside the call (qlora_mx_quantize); the adapter reads X itself:
+ *   Y = deq(Q(X)) deq(W)^T + s (X' A^T) B^T,  T_save = RNbf16(X' A^T),
+ * s = alpha / r, X' = X, or dropout(X) when `dropout` is not NULL.  Arguments
+ * as for qlora_linear_fwd_dropout; r = 0 with A, B, T_save and dropout NULL is
+ * the layer without an adapter.  The adapter runs in the product's own
+ * accumulator: with NVFP4 its bf16 factors are divided by the row scales
+ * (exact for powers of two).
+ * Constraints: M >= 1, N % 8 == 0, K % 64 == 0, r in {0, 8, 16, 32, 64, 128},
+ * ws of qlora_workspace_bytes(QLORA_OP_MX_FWD, M, N, K, r) bytes.
+ */
+int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, const void* A,
+                        const void* B, int r, float alpha, const qlora_dropout* dropout, void* Y,
+                        void* T_save, void* ws, size_t ws_bytes, qlora_stream_t stream);
+
+/*
+ * Its backward.  The quantisation of X is passed straight through:
+ *   dX = dY deq(W) + D c (s U A),  U = dY B,  dA = s U^T X',  dB = s dY^T T
+ * with the bf16 values of qlora_mx_dequantize for deq(W); arguments as for
+ * qlora_linear_bwd_dropout, `dropout` may be NULL, r = 0 (A, B, T, dA, dB and
+ * dropout NULL) computes dX alone.  T is the forward's T_save, or NULL to
+ * recompute it.  ws of qlora_workspace_bytes(QLORA_OP_MX_BWD, M, N, K, r) bytes.
+ */
+int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY, int64_t M,
+                        const void* A, const void* B, int r, float alpha,
+                        const qlora_dropout* dropout, const void* T, void* dX, void* dA, void* dB,
+                        void* ws, size_t ws_bytes, qlora_stream_t stream);
+
+/*
+ * Dropout as a call of its own, with the mask of the layer's dropout (see
+ * qlora_dropout), which is never stored:
+ *   forward   Y  = RN(RN32(D c X) + R)     R NULL: Y = RN(D c X)
+ *   backward  dX = RN(D c dY)              (R's gradient is dY)
+ * over [rows, cols] of one dtype, fp32 or bf16, rows ldx / ldr / ldy elements
+ * apart.  Element (i, j) has number first + i * cols + j in the mask, so parts
+ * of a tensor processed apart get the whole tensor's mask; with first = 0 and
+ * bf16, forward(X) is the X' of the layer called with the same p and seed.
+ * A dropped element is 0 whatever X holds.  The output may be an input.
+ */
+int qlora_dropout_fwd(const void* X, int64_t ldx, const void* R, int64_t ldr, int dtype,
+                      int64_t rows, int64_t cols, const qlora_dropout* dropout, int64_t first,
+                      void* Y, int64_t ldy, qlora_stream_t stream);
+int qlora_dropout_bwd(const void* dY, int64_t ldy, int dtype, int64_t rows, int64_t cols,
+                      const qlora_dropout* dropout, int64_t first, void* dX, int64_t ldx,
+                      qlora_stream_t stream);
 
 /*
  * Forward without a workspace argument, for callers that cannot allocate

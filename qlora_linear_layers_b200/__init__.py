@@ -6,11 +6,15 @@ in the library's sm_100a kernels.  The functions named like the C entry
 points (nf4_quantize, nf4_double_quantize, nf4_dequantize, qlora_linear_fwd,
 qlora_linear_bwd, qlora_check_status) marshal tensors to pointers; `quantize`,
 `dequantize`, `linear_fwd`, `linear_bwd` are conveniences that allocate the
-outputs and the workspace with torch and call them.
+outputs and the workspace with torch and call them.  The microscaled 4-bit
+formats (`mx_quantize`, `mx_dequantize`, `mx_matmul`, `mx_linear_fwd`,
+`mx_linear_bwd`) and the standalone dropout (`dropout_fwd`, `dropout_bwd`) have
+the same two layers.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 from dataclasses import dataclass
 
@@ -64,6 +68,41 @@ class NF4Tensor:
             return (self.packed.numel() + self.qabsmax.numel() + 4 * self.dq_scale.numel()
                     + 4 * self.dq_mean.numel())
         return self.packed.numel() + 4 * self.absmax.numel()
+
+
+@dataclass
+class MXTensor:
+    """A microscaled 4-bit matrix: the buffers of `qlora_mx_tensor` plus its shape."""
+    packed: torch.Tensor            # uint8 [rows*cols/2], element 2j in the low nibble
+    scales: torch.Tensor            # uint8, tiles of 128 rows x 4 scale columns
+    row_scale: torch.Tensor | None  # fp32 [rows] (NVFP4)
+    rows: int
+    cols: int
+    format: int = _lib.QLORA_NVFP4
+
+    def c_struct(self) -> _lib.MXTensor:
+        _need_cuda(self.packed, self.scales, self.row_scale)
+        if (self.packed.numel() != self.rows * self.cols // 2
+                or self.scales.numel() < mx_scale_bytes(self.format, self.rows, self.cols)
+                or self.format == _lib.QLORA_NVFP4 and (self.row_scale is None
+                                                        or self.row_scale.numel() != self.rows)):
+            raise ValueError("buffers do not fit a %d x %d matrix of format %d"
+                             % (self.rows, self.cols, self.format))
+        return _lib.MXTensor(packed=_ptr(self.packed), rows=self.rows, cols=self.cols,
+                             format=self.format, reserved=0, scales=_ptr(self.scales),
+                             row_scale=_ptr(self.row_scale))
+
+    def block_scales(self) -> torch.Tensor:
+        """The scale bytes as a row-major [rows, cols / block] tensor (a copy)."""
+        n = self.cols // (16 if self.format == _lib.QLORA_NVFP4 else 32)
+        rb, tiles = (self.rows + 127) // 128, (n + 3) // 4
+        t = self.scales[:rb * tiles * 512].view(rb, tiles, 32, 4, 4).permute(0, 3, 2, 1, 4)
+        return t.reshape(rb * 128, tiles * 4)[:self.rows, :n].contiguous()
+
+    def stored_bytes(self) -> int:
+        """Bytes the quantised matrix occupies."""
+        rs = 4 * self.rows if self.format == _lib.QLORA_NVFP4 else 0
+        return self.packed.numel() + self.scales.numel() + rs
 
 
 # ---------------------------------------------------------------------------
@@ -205,6 +244,157 @@ def qlora_linear_bwd_dropout(w: NF4Tensor, X, dY, A, B, alpha: float, p: float, 
                "qlora_linear_bwd_dropout")
 
 
+def _need_rows(*ts):
+    """2-D CUDA tensors whose rows are contiguous (any row stride)."""
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)
+                              or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
+            raise ValueError("tensors must be 2-D CUDA tensors with contiguous rows")
+
+
+def _ld(t) -> int:
+    return 0 if t is None else max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+
+
+def _place(stream, *ts):
+    """Context in which a call's buffers are allocated and its work enqueued:
+    the tensors' device (all on one), and `stream` when it is given, so that
+    the allocator orders the buffers' reuse after that stream's work."""
+    ts = [t for t in ts if t is not None]
+    if any(t.device != ts[0].device for t in ts):
+        raise ValueError("tensors are on different devices")
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if ts[0].is_cuda and ts[0].device.index != torch.cuda.current_device():
+        return torch.cuda.device(ts[0].device)
+    return contextlib.nullcontext()
+
+
+def _need_shape(*pairs):
+    for t, shape in pairs:
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_dtype(dtype, *ts):
+    for t in ts:
+        if t is not None and t.dtype != dtype:
+            raise ValueError(f"expected {dtype}, got {t.dtype}")
+
+
+def _float_type(t) -> int:
+    dt = {torch.float32: _lib.QLORA_F32, torch.bfloat16: _lib.QLORA_BF16}.get(t.dtype)
+    if dt is None:
+        raise ValueError("expected fp32 or bf16")
+    return dt
+
+
+def mx_scale_bytes(format: int, rows: int, cols: int) -> int:
+    return int(_lib.load().qlora_mx_scale_bytes(int(format), rows, cols))
+
+
+def qlora_mx_quantize(X: torch.Tensor, out: MXTensor, stream=None):
+    """Quantise X (fp32/bf16, rows contiguous, any row stride) into `out`."""
+    _need_rows(X)
+    _need_shape((X, (out.rows, out.cols)))
+    cw = out.c_struct()
+    with _place(stream, X, out.packed, out.scales, out.row_scale):
+        _lib.check(_lib.load().qlora_mx_quantize(_ptr(X), _float_type(X), out.rows, out.cols, _ld(X),
+                                                 int(out.format), cw.packed, cw.scales, cw.row_scale,
+                                                 _stream(stream)),
+                   "qlora_mx_quantize")
+
+
+def qlora_mx_dequantize(t: MXTensor, out: torch.Tensor, stream=None):
+    _need_cuda(out)
+    _need_shape((out, (t.rows, t.cols)))
+    _need_dtype(torch.bfloat16, out)
+    cw = t.c_struct()
+    with _place(stream, out, t.packed, t.scales, t.row_scale):
+        _lib.check(_lib.load().qlora_mx_dequantize(C.byref(cw), _ptr(out), _stream(stream)),
+                   "qlora_mx_dequantize")
+
+
+def qlora_mx_matmul(x: MXTensor, w: MXTensor, Y: torch.Tensor, stream=None):
+    """Y[M, N] bf16 = deq(x) deq(w)^T, both of one format."""
+    _need_cuda(Y)
+    _need_shape((Y, (x.rows, w.rows)))
+    _need_dtype(torch.bfloat16, Y)
+    cx, cw = x.c_struct(), w.c_struct()
+    with _place(stream, Y, x.packed, x.scales, x.row_scale, w.packed, w.scales, w.row_scale):
+        _lib.check(_lib.load().qlora_mx_matmul(C.byref(cx), C.byref(cw), _ptr(Y), _stream(stream)),
+                   "qlora_mx_matmul")
+
+
+def _mx_dropout(p: float, seed: int):
+    return None if p == 0 else C.byref(_lib.Dropout(p=float(p), reserved=0, seed=int(seed)))
+
+
+def qlora_mx_linear_fwd(w: MXTensor, X, A, B, alpha: float, Y, T_save=None, p: float = 0.0,
+                        seed: int = 0, ws=None, stream=None):
+    """The QLoRA layer on a microscaled base (A = B = None: no adapter)."""
+    _need_cuda(X, A, B, Y, T_save)
+    _need_dtype(torch.bfloat16, X, A, B, Y, T_save)
+    M, r = X.shape[0], 0 if A is None else A.shape[0]
+    _need_shape((X, (M, w.cols)), (A, (r, w.cols)), (B, (w.rows, r)), (Y, (M, w.rows)),
+                (T_save, (M, r)))
+    with _place(stream, X, A, B, Y, T_save, w.packed, w.scales, w.row_scale):
+        if ws is None:
+            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_FWD, M, w.rows, w.cols, r), X.device)
+        cw = w.c_struct()
+        _lib.check(_lib.load().qlora_mx_linear_fwd(C.byref(cw), _ptr(X), M, _ptr(A), _ptr(B), r,
+                                                   float(alpha), _mx_dropout(p, seed), _ptr(Y),
+                                                   _ptr(T_save), _ptr(ws), ws.numel(),
+                                                   _stream(stream)),
+                   "qlora_mx_linear_fwd")
+
+
+def qlora_mx_linear_bwd(w: MXTensor, X, dY, A, B, alpha: float, dX, dA, dB, T=None,
+                        p: float = 0.0, seed: int = 0, ws=None, stream=None):
+    """Its backward (A = B = dA = dB = None: dX alone)."""
+    _need_cuda(X, dY, A, B, dX, dA, dB, T)
+    _need_dtype(torch.bfloat16, X, dY, A, B, dX, dA, dB, T)
+    M, r = X.shape[0], 0 if A is None else A.shape[0]
+    _need_shape((X, (M, w.cols)), (dY, (M, w.rows)), (A, (r, w.cols)), (B, (w.rows, r)),
+                (dX, (M, w.cols)), (dA, (r, w.cols)), (dB, (w.rows, r)), (T, (M, r)))
+    with _place(stream, X, dY, A, B, dX, dA, dB, T, w.packed, w.scales, w.row_scale):
+        if ws is None:
+            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_BWD, M, w.rows, w.cols, r), X.device)
+        cw = w.c_struct()
+        _lib.check(_lib.load().qlora_mx_linear_bwd(C.byref(cw), _ptr(X), _ptr(dY), M, _ptr(A), _ptr(B),
+                                                   r, float(alpha), _mx_dropout(p, seed), _ptr(T),
+                                                   _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
+                                                   _stream(stream)),
+                   "qlora_mx_linear_bwd")
+
+
+def qlora_dropout_fwd(X, p: float, seed: int, Y, residual=None, first: int = 0, stream=None):
+    """Y = dropout(X) + residual with the layer's mask; element (i, j) has
+    number first + i * cols + j.  Y may be X or residual."""
+    _need_rows(X, Y, residual)
+    _need_shape((Y, X.shape), (residual, X.shape))
+    _need_dtype(X.dtype, Y, residual)
+    dr = _lib.Dropout(p=float(p), reserved=0, seed=int(seed))
+    with _place(stream, X, Y, residual):
+        _lib.check(_lib.load().qlora_dropout_fwd(_ptr(X), _ld(X), _ptr(residual), _ld(residual),
+                                                 _float_type(X), X.shape[0], X.shape[1], C.byref(dr),
+                                                 int(first), _ptr(Y), _ld(Y), _stream(stream)),
+                   "qlora_dropout_fwd")
+
+
+def qlora_dropout_bwd(dY, p: float, seed: int, dX, first: int = 0, stream=None):
+    """dX = D c dY with the forward's mask, regenerated."""
+    _need_rows(dY, dX)
+    _need_shape((dX, dY.shape))
+    _need_dtype(dY.dtype, dX)
+    dr = _lib.Dropout(p=float(p), reserved=0, seed=int(seed))
+    with _place(stream, dY, dX):
+        _lib.check(_lib.load().qlora_dropout_bwd(_ptr(dY), _ld(dY), _float_type(dY), dY.shape[0],
+                                                 dY.shape[1], C.byref(dr), int(first), _ptr(dX),
+                                                 _ld(dX), _stream(stream)),
+                   "qlora_dropout_bwd")
+
+
 def qlora_check_status(stream=None) -> int:
     """Synchronise the stream; return and clear the device status word."""
     return int(_lib.load().qlora_check_status(_stream(stream)))
@@ -307,3 +497,73 @@ def linear_bwd(w: NF4Tensor, X, dY, A, B, alpha: float, T=None, stream=None):
     dB = torch.empty_like(B)
     qlora_linear_bwd(w, X, dY, A, B, alpha, dX, dA, dB, T=T, stream=stream)
     return dX, dA, dB
+
+
+def mx_empty(rows: int, cols: int, device, format: int = _lib.QLORA_NVFP4) -> MXTensor:
+    """Buffers of a microscaled [rows, cols] matrix."""
+    nv = format == _lib.QLORA_NVFP4
+    return MXTensor(torch.empty(rows * cols // 2, dtype=torch.uint8, device=device),
+                    torch.empty(mx_scale_bytes(format, rows, cols), dtype=torch.uint8, device=device),
+                    torch.empty(rows, dtype=torch.float32, device=device) if nv else None,
+                    rows, cols, int(format))
+
+
+def mx_quantize(X: torch.Tensor, format: int = _lib.QLORA_NVFP4, stream=None) -> MXTensor:
+    """Quantise a weight or activations: format 0 MXFP4, 1 NVFP4."""
+    _need_rows(X)
+    with _place(stream, X):
+        t = mx_empty(X.shape[0], X.shape[1], X.device, format)
+    qlora_mx_quantize(X, t, stream)
+    return t
+
+
+def mx_dequantize(t: MXTensor, stream=None) -> torch.Tensor:
+    with _place(stream, t.packed):
+        out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.packed.device)
+    qlora_mx_dequantize(t, out, stream)
+    return out
+
+
+def mx_matmul(x: MXTensor, w: MXTensor, stream=None) -> torch.Tensor:
+    with _place(stream, x.packed):
+        Y = torch.empty(x.rows, w.rows, dtype=torch.bfloat16, device=x.packed.device)
+    qlora_mx_matmul(x, w, Y, stream)
+    return Y
+
+
+def mx_linear_fwd(w: MXTensor, X, A=None, B=None, alpha: float = 0.0, p: float = 0.0, seed: int = 0,
+                  save_T: bool = True, stream=None):
+    """(Y, T) of the layer on a microscaled base; T is None without an adapter."""
+    T = None
+    with _place(stream, X):
+        Y = torch.empty(X.shape[0], w.rows, dtype=torch.bfloat16, device=X.device)
+        if A is not None and save_T:
+            T = torch.empty(X.shape[0], A.shape[0], dtype=torch.bfloat16, device=X.device)
+    qlora_mx_linear_fwd(w, X, A, B, alpha, Y, T, p, seed, stream=stream)
+    return Y, T
+
+
+def mx_linear_bwd(w: MXTensor, X, dY, A=None, B=None, alpha: float = 0.0, p: float = 0.0,
+                  seed: int = 0, T=None, stream=None):
+    """(dX, dA, dB); dA and dB are None without an adapter."""
+    with _place(stream, X):
+        dX = torch.empty_like(X)
+        dA = None if A is None else torch.empty_like(A)
+        dB = None if B is None else torch.empty_like(B)
+    qlora_mx_linear_bwd(w, X, dY, A, B, alpha, dX, dA, dB, T, p, seed, stream=stream)
+    return dX, dA, dB
+
+
+def dropout_fwd(X, p: float, seed: int, residual=None, first: int = 0, stream=None) -> torch.Tensor:
+    """dropout(X) (+ residual) with the mask of the layer's dropout."""
+    with _place(stream, X):
+        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
+    qlora_dropout_fwd(X, p, seed, Y, residual, first, stream)
+    return Y
+
+
+def dropout_bwd(dY, p: float, seed: int, first: int = 0, stream=None) -> torch.Tensor:
+    with _place(stream, dY):
+        dX = torch.empty(dY.shape, dtype=dY.dtype, device=dY.device)
+    qlora_dropout_bwd(dY, p, seed, dX, first, stream)
+    return dX

@@ -39,6 +39,12 @@ QLORA_OP_BWD = 2
 QLORA_OP_FWD_DROPOUT = 3
 QLORA_OP_BWD_DROPOUT = 4
 
+QLORA_OP_MX_FWD = 5
+QLORA_OP_MX_BWD = 6
+
+QLORA_MXFP4 = 0
+QLORA_NVFP4 = 1
+
 QLORA_FWD_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 # Every symbol the header declares, with (restype, argtypes).
@@ -59,6 +65,19 @@ class NF4Weight(C.Structure):
         ("dq_mean", _vp),
         ("dq_blocksize", C.c_int32),
         ("quant_type", C.c_int32),
+    ]
+
+
+class MXTensor(C.Structure):
+    """Mirror of `qlora_mx_tensor` in include/qlora_nf4.h."""
+    _fields_ = [
+        ("packed", _vp),
+        ("rows", _i64),
+        ("cols", _i64),
+        ("format", C.c_int32),
+        ("reserved", C.c_int32),
+        ("scales", _vp),
+        ("row_scale", _vp),
     ]
 
 
@@ -95,6 +114,18 @@ SIGNATURES = {
                                         C.POINTER(Dropout), _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "qlora_linear_fwd_noalloc": (_i32, [C.POINTER(NF4Weight), _vp, _i64, _vp, _vp, _i32, _f32,
                                         _vp, _vp, _vp]),
+    "qlora_mx_scale_bytes": (_sz, [_i32, _i64, _i64]),
+    "qlora_mx_quantize": (_i32, [_vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]),
+    "qlora_mx_dequantize": (_i32, [C.POINTER(MXTensor), _vp, _vp]),
+    "qlora_mx_matmul": (_i32, [C.POINTER(MXTensor), C.POINTER(MXTensor), _vp, _vp]),
+    "qlora_mx_linear_fwd": (_i32, [C.POINTER(MXTensor), _vp, _i64, _vp, _vp, _i32, _f32,
+                                   C.POINTER(Dropout), _vp, _vp, _vp, _sz, _vp]),
+    "qlora_mx_linear_bwd": (_i32, [C.POINTER(MXTensor), _vp, _vp, _i64, _vp, _vp, _i32, _f32,
+                                   C.POINTER(Dropout), _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "qlora_dropout_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, C.POINTER(Dropout), _i64,
+                                 _vp, _i64, _vp]),
+    "qlora_dropout_bwd": (_i32, [_vp, _i64, _i32, _i64, _i64, C.POINTER(Dropout), _i64, _vp, _i64,
+                                 _vp]),
     "qlora_check_status": (_i32, [_vp]),
     "qlora_set_wait_limit": (_i32, [C.c_uint64]),
     "qlora_test_withhold_first_fill": (_i32, [_i32]),

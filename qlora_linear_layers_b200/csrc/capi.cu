@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "gemm.h"
+#include "mx.h"
 
 namespace qnf4 {
 
@@ -110,9 +111,46 @@ BwdWs bwd_ws(int64_t M, int64_t N, int64_t K, int r) {
   return w;
 }
 
+// Forward workspace of the layer on a microscaled base: the quantised tokens
+// (codes, scale tiles, row scales), then the adapter's factors as in FwdWs,
+// both padded (NVFP4 also divides them by the row scales); r = 0 has none.
+struct MxFwdWs {
+  size_t xq, xs, xr, sT, Bpad, part, total;
+};
+MxFwdWs mx_fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
+  MxFwdWs w{};
+  size_t off = 0;
+  w.xq = off; off += align256((size_t)M * K / 2);
+  w.xs = off; off += align256((size_t)((M + 127) / 128) * mx_scale_tiles(QLORA_NVFP4, K) * 512);
+  w.xr = off; off += align256((size_t)M * 4);
+  if (r) {
+    const int RP = padded_rank(r);
+    w.sT = off;   off += align256((size_t)M * RP * 2);
+    w.Bpad = off; off += align256((size_t)N * RP * 2);
+    w.part = off; off += align256(skinny_workspace_bytes((int)M, (int)K, RP));
+  }
+  w.total = off;
+  return w;
+}
+
 int launch_status() {
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+bool valid_alpha(float a) { return a == a && a <= 3.0e38f && a >= -3.0e38f; }
+
+bool valid_mx_format(int f) { return f == QLORA_MXFP4 || f == QLORA_NVFP4; }
+
+int check_mx(const qlora_mx_tensor* t) {
+  if (!t || !t->packed || !t->scales) return QLORA_ERR_INVALID_ARG;
+  if (!valid_mx_format(t->format)) return QLORA_ERR_INVALID_ARG;
+  if (t->format == QLORA_NVFP4 && !t->row_scale) return QLORA_ERR_INVALID_ARG;
+  if (t->rows < 1 || t->cols < 32 || t->cols % 32 || t->rows > (1 << 30) || t->cols > (1 << 30))
+    return QLORA_ERR_SHAPE;
+  if (!aligned16(t->packed) || !aligned16(t->scales) || (t->format == QLORA_NVFP4 && !aligned16(t->row_scale)))
+    return QLORA_ERR_ALIGN;
+  return QLORA_OK;
 }
 
 int check_weight(const nf4_weight* w) {
@@ -290,6 +328,12 @@ size_t qlora_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r) {
     case QLORA_OP_FWD_DROPOUT:
       if (M < 1 || N < 1 || K < 1 || !valid_rank(r)) return 0;
       return fwd_ws(M, N, K, r, true).total;
+    case QLORA_OP_MX_FWD:
+      if (M < 1 || N < 1 || K < 1 || (r && !valid_rank(r))) return 0;
+      return mx_fwd_ws(M, N, K, r).total;
+    case QLORA_OP_MX_BWD:
+      if (M < 1 || N < 1 || K < 1 || (r && !valid_rank(r))) return 0;
+      return r ? bwd_ws(M, N, K, r).total : align256((size_t)K * N * 2);
     default: return 0;
   }
 }
@@ -470,41 +514,32 @@ static int fwd_impl(const nf4_weight* w, const void* X, int64_t M, const void* A
   return st;
 }
 
-static int bwd_impl(const nf4_weight* w, const void* X, const void* dY, int64_t M, const void* A,
-                    const void* B, int r, float alpha, const Dropout* drop, const void* T, void* dX,
-                    void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
-  int st = check_weight(w);
-  if (st) return st;
-  if (!X || !dY || !A || !B || !dX || !dA || !dB) return QLORA_ERR_INVALID_ARG;
-  if (!valid_rank(r) || !(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f) return QLORA_ERR_INVALID_ARG;
-  const int64_t N = w->rows, K = w->cols;
-  if (M < 1 || N % 8 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return QLORA_ERR_SHAPE;
-  if (!aligned16(X) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
-      !aligned16(dA) || !aligned16(dB) || (T && !aligned16(T)))
-    return QLORA_ERR_ALIGN;
-  const BwdWs lay = bwd_ws(M, N, K, r);
-  if (!ws || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
-  DeviceInfo* d = nullptr;
-  st = current_device(&d);
-  if (st) return st;
+}  // extern "C"
+
+// The backward after its argument checks: w_t writes deq(W)^T [K, N] in bf16.
+// r = 0 (microscaled layer without an adapter) computes dX = dY W' alone.
+template <typename DequantT>
+static int bwd_run(DequantT&& w_t, int64_t N, int64_t K, const void* X, const void* dY, int64_t M,
+                   const void* A, const void* B, int r, float alpha, const Dropout* drop, const void* T,
+                   void* dX, void* dA, void* dB, void* ws, qlora_stream_t stream, DeviceInfo* d) {
+  const BwdWs lay = r ? bwd_ws(M, N, K, r) : BwdWs{};
   cudaStream_t s = (cudaStream_t)stream;
-  const int RP = padded_rank(r);
-  const float scale = alpha / (float)r;
+  const int RP = r ? padded_rank(r) : 0;
+  const float scale = r ? alpha / (float)r : 0.0f;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   void* Tw = wsb + lay.T;
   void* sU = wsb + lay.sU;
   void* Wt = wsb + lay.Wt;
   void* At = wsb + lay.At;
-  int n = 7;   // dequant_t, transpose_pad, GEMM, 2 x (partials + reduce)
-  if (!T) {
+  int n = r ? 7 : 2;   // dequant_t, transpose_pad, GEMM, 2 x (partials + reduce)
+  if (r && !T) {
     n += launch_lora_down(X, A, (int)M, (int)K, r, RP, scale, nullptr, Tw,
                           reinterpret_cast<float*>(wsb + lay.pT), s, drop);
     T = Tw;
   }
-  n += launch_lora_u(dY, B, (int)M, (int)N, r, RP, scale, sU, reinterpret_cast<float*>(wsb + lay.pU), s);
-  launch_dequant_t(w, Wt, s);
-  launch_transpose_pad(A, r, (int)K, RP, At, s);
+  if (r) n += launch_lora_u(dY, B, (int)M, (int)N, r, RP, scale, sU, reinterpret_cast<float*>(wsb + lay.pU), s);
+  w_t(Wt, s);
+  if (r) launch_transpose_pad(A, r, (int)K, RP, At, s);
   // dX[M, K] = dY Wt^T + sU At^T   (tokens = dY rows, outputs = K, contraction = N)
   GemmArgs a{};
   a.out = static_cast<__nv_bfloat16*>(dX);
@@ -519,23 +554,48 @@ static int bwd_impl(const nf4_weight* w, const void* X, const void* dY, int64_t 
   cudaEvent_t e0, e1;
   take_gemm_events(&e0, &e1);
   if (e0) cudaEventRecord(e0, s);
-  st = K > 128 ? launch_qlora_gemm_pair(a, dY, sU, At, Wt, RP, s, d->sms)
-               : launch_qlora_gemm(MODE_BF16, a, dY, sU, At, Wt, RP, s, d->sms);
+  int st = K > 128 ? launch_qlora_gemm_pair(a, dY, r ? sU : dY, r ? At : Wt, Wt, r ? RP : 64, s, d->sms)
+                   : launch_qlora_gemm(MODE_BF16, a, dY, r ? sU : dY, r ? At : Wt, Wt, r ? RP : 64, s, d->sms);
   if (e1) cudaEventRecord(e1, s);
   if (st) return st;
-  if (dropping) {
-    launch_rank_add(sU, RP, A, r, (int)M, (int)K, dX, *drop, s);
-    ++n;
+  if (r) {
+    if (dropping) {
+      launch_rank_add(sU, RP, A, r, (int)M, (int)K, dX, *drop, s);
+      ++n;
+    }
+    // dA[r, K] = (s U)^T X ;  dB[N, r] = s dY^T T
+    launch_atb(sU, RP, r, X, (int)K, (int)K, (int)M, 1.0f, dA, reinterpret_cast<float*>(wsb + lay.pA),
+               d->sms, s, drop);
+    launch_atb(dY, (int)N, (int)N, T, r, r, (int)M, scale, dB, reinterpret_cast<float*>(wsb + lay.pB),
+               d->sms, s);
   }
-  // dA[r, K] = (s U)^T X ;  dB[N, r] = s dY^T T
-  launch_atb(sU, RP, r, X, (int)K, (int)K, (int)M, 1.0f, dA, reinterpret_cast<float*>(wsb + lay.pA),
-             d->sms, s, drop);
-  launch_atb(dY, (int)N, (int)N, T, r, r, (int)M, scale, dB, reinterpret_cast<float*>(wsb + lay.pB),
-             d->sms, s);
   st = launch_status();
   if (!st) count_launches(n);
   return st;
 }
+
+static int bwd_impl(const nf4_weight* w, const void* X, const void* dY, int64_t M, const void* A,
+                    const void* B, int r, float alpha, const Dropout* drop, const void* T, void* dX,
+                    void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  int st = check_weight(w);
+  if (st) return st;
+  if (!X || !dY || !A || !B || !dX || !dA || !dB) return QLORA_ERR_INVALID_ARG;
+  if (!valid_rank(r) || !(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f) return QLORA_ERR_INVALID_ARG;
+  const int64_t N = w->rows, K = w->cols;
+  if (M < 1 || N % 8 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return QLORA_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
+      !aligned16(dA) || !aligned16(dB) || (T && !aligned16(T)))
+    return QLORA_ERR_ALIGN;
+  if (!ws || ws_bytes < bwd_ws(M, N, K, r).total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
+  return bwd_run([&](void* Wt, cudaStream_t s) { launch_dequant_t(w, Wt, s); }, N, K, X, dY, M, A, B, r,
+                 alpha, drop, T, dX, dA, dB, ws, stream, d);
+}
+
+extern "C" {
 
 int qlora_linear_fwd(const nf4_weight* w, const void* X, int64_t M, const void* A, const void* B,
                      int r, float alpha, void* Y, void* T_save, void* ws, size_t ws_bytes,
@@ -578,6 +638,181 @@ int qlora_linear_bwd_dropout(const nf4_weight* w, const void* X, const void* dY,
   const int st = make_dropout(dropout, &dr);
   if (st) return st;
   return bwd_impl(w, X, dY, M, A, B, r, alpha, &dr, T, dX, dA, dB, ws, ws_bytes, stream);
+}
+
+size_t qlora_mx_scale_bytes(int format, int64_t rows, int64_t cols) {
+  if (!valid_mx_format(format) || rows < 1 || cols < 32 || cols % 32) return 0;
+  return (size_t)((rows + 127) / 128) * (size_t)mx_scale_tiles(format, cols) * 512;
+}
+
+int qlora_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
+                      uint8_t* packed, uint8_t* scales, float* row_scale, qlora_stream_t stream) {
+  if (!X || !packed || !scales || !valid_mx_format(format)) return QLORA_ERR_INVALID_ARG;
+  if (format == QLORA_NVFP4 && !row_scale) return QLORA_ERR_INVALID_ARG;
+  if (dtype != QLORA_F32 && dtype != QLORA_BF16) return QLORA_ERR_INVALID_ARG;
+  if (rows < 1 || cols < 32 || cols % 32 || rows > (1 << 30) || cols > (1 << 30) || ld < cols ||
+      ld % (dtype == QLORA_F32 ? 4 : 8) || ld > ((int64_t)1 << 40) / rows)
+    return QLORA_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(packed) || !aligned16(scales) || (row_scale && !aligned16(row_scale)))
+    return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  int st = current_device(&d);
+  if (st) return st;
+  launch_mx_quantize(X, dtype, rows, cols, ld, format, packed, scales, row_scale, d->status, (cudaStream_t)stream);
+  st = launch_status();
+  if (!st) count_launches(1);
+  return st;
+}
+
+int qlora_mx_dequantize(const qlora_mx_tensor* t, void* out, qlora_stream_t stream) {
+  int st = check_mx(t);
+  if (st) return st;
+  if (!out) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(out)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
+  launch_mx_dequantize(t, out, (cudaStream_t)stream);
+  st = launch_status();
+  if (!st) count_launches(1);
+  return st;
+}
+
+int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y, qlora_stream_t stream) {
+  int st = check_mx(x);
+  if (!st) st = check_mx(w);
+  if (st) return st;
+  if (!Y || x->format != w->format) return QLORA_ERR_INVALID_ARG;
+  if (x->cols != w->cols) return QLORA_ERR_SHAPE;
+  if (!aligned16(Y)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
+  st = launch_mx_gemm(x, w, nullptr, nullptr, 0, Y, d->status, (cudaStream_t)stream, d->sms);
+  if (st) return st;
+  st = launch_status();
+  if (!st) count_launches(1);
+  return st;
+}
+
+// Checks that the layer's forward and backward share.
+static int check_mx_layer(const qlora_mx_tensor* w, const void* X, int64_t M, const void* A, const void* B,
+                          int r, float alpha, const qlora_dropout* dropout, Dropout* dr) {
+  int st = check_mx(w);
+  if (st) return st;
+  if (!X || (r ? !A || !B : A || B)) return QLORA_ERR_INVALID_ARG;
+  if ((r && !valid_rank(r)) || !valid_alpha(alpha)) return QLORA_ERR_INVALID_ARG;
+  if (dropout) {
+    st = make_dropout(dropout, dr);
+    if (st) return st;
+    if (!r) return QLORA_ERR_INVALID_ARG;          // dropout acts on the adapter's input
+  }
+  if (M < 1 || M > (1 << 30) || w->rows % 8 || w->cols % 64) return QLORA_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B)) return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, const void* A, const void* B,
+                        int r, float alpha, const qlora_dropout* dropout, void* Y, void* T_save, void* ws,
+                        size_t ws_bytes, qlora_stream_t stream) {
+  Dropout dr{};
+  int st = check_mx_layer(w, X, M, A, B, r, alpha, dropout, &dr);
+  if (st) return st;
+  if (!Y || (!r && T_save)) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(Y) || !aligned16(T_save)) return QLORA_ERR_ALIGN;
+  const int64_t N = w->rows, K = w->cols;
+  const MxFwdWs lay = mx_fwd_ws(M, N, K, r);
+  if (!ws || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  const bool nv = w->format == QLORA_NVFP4;
+  float* xr = nv ? reinterpret_cast<float*>(wsb + lay.xr) : nullptr;
+  launch_mx_quantize(X, QLORA_BF16, M, K, K, w->format, wsb + lay.xq, wsb + lay.xs, xr, d->status, s);
+  int n = 2;
+  const void* Bp = B;
+  const int RP = r ? padded_rank(r) : 0;
+  if (r) {
+    void* sT = wsb + lay.sT;
+    n += launch_lora_down(X, A, (int)M, (int)K, r, RP, alpha / (float)r, sT, T_save,
+                          reinterpret_cast<float*>(wsb + lay.part), s, dropout ? &dr : nullptr);
+    if (nv) {
+      launch_mx_pad_rows(sT, M, RP, RP, RP, xr, sT, s);
+      ++n;
+    }
+    if (nv || r < RP) {
+      launch_mx_pad_rows(B, N, r, r, RP, nv ? w->row_scale : nullptr, wsb + lay.Bpad, s);
+      Bp = wsb + lay.Bpad;
+      ++n;
+    }
+  }
+  qlora_mx_tensor x{};
+  x.packed = wsb + lay.xq;
+  x.rows = M; x.cols = K;
+  x.format = w->format;
+  x.scales = wsb + lay.xs;
+  x.row_scale = xr;
+  cudaEvent_t e0, e1;
+  take_gemm_events(&e0, &e1);
+  if (e0) cudaEventRecord(e0, s);
+  st = launch_mx_gemm(&x, w, r ? wsb + lay.sT : nullptr, r ? Bp : nullptr, RP, Y, d->status, s, d->sms);
+  if (e1) cudaEventRecord(e1, s);
+  if (st) return st;
+  st = launch_status();
+  if (!st) count_launches(n);
+  return st;
+}
+
+int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY, int64_t M, const void* A,
+                        const void* B, int r, float alpha, const qlora_dropout* dropout, const void* T,
+                        void* dX, void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  Dropout dr{};
+  int st = check_mx_layer(w, X, M, A, B, r, alpha, dropout, &dr);
+  if (st) return st;
+  if (!dY || !dX || (r ? !dA || !dB : dA || dB || T)) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(dY) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) || !aligned16(T)) return QLORA_ERR_ALIGN;
+  if (!ws || ws_bytes < qlora_workspace_bytes(QLORA_OP_MX_BWD, M, w->rows, w->cols, r)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
+  return bwd_run([&](void* Wt, cudaStream_t s) { launch_mx_dequant_t(w, Wt, s); }, w->rows, w->cols, X, dY, M,
+                 A, B, r, alpha, dropout ? &dr : nullptr, T, dX, dA, dB, ws, stream, d);
+}
+
+static int dropout_impl(const void* X, int64_t ldx, const void* R, int64_t ldr, int dtype, int64_t rows,
+                        int64_t cols, const qlora_dropout* dropout, int64_t first, void* Y, int64_t ldy,
+                        qlora_stream_t stream) {
+  Dropout dr{};
+  int st = make_dropout(dropout, &dr);
+  if (st) return st;
+  if (!X || !Y || (dtype != QLORA_F32 && dtype != QLORA_BF16)) return QLORA_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 40;
+  if (rows < 1 || cols < 1 || cols > most || rows > most / cols || ldx < cols || ldy < cols || (R && ldr < cols) ||
+      ldx > most || ldy > most || (R && ldr > most) || first < 0 || first > ((int64_t)1 << 62))
+    return QLORA_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(R)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
+  launch_dropout(X, ldx, R, ldr, Y, ldy, dtype, rows, cols, first, dr, (cudaStream_t)stream);
+  st = launch_status();
+  if (!st) count_launches(1);
+  return st;
+}
+
+int qlora_dropout_fwd(const void* X, int64_t ldx, const void* R, int64_t ldr, int dtype, int64_t rows,
+                      int64_t cols, const qlora_dropout* dropout, int64_t first, void* Y, int64_t ldy,
+                      qlora_stream_t stream) {
+  return dropout_impl(X, ldx, R, ldr, dtype, rows, cols, dropout, first, Y, ldy, stream);
+}
+
+int qlora_dropout_bwd(const void* dY, int64_t ldy, int dtype, int64_t rows, int64_t cols,
+                      const qlora_dropout* dropout, int64_t first, void* dX, int64_t ldx, qlora_stream_t stream) {
+  return dropout_impl(dY, ldy, nullptr, 0, dtype, rows, cols, dropout, first, dX, ldx, stream);
 }
 
 // Write one field of the current device's state block (synchronous).

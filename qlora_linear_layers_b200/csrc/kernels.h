@@ -33,6 +33,12 @@ void launch_dequantize(const nf4_weight* w, void* out, cudaStream_t s, int num_s
 void launch_merge(const nf4_weight* w, const void* A, const void* B, int r, float s, void* out,
                   cudaStream_t st);
 
+struct Dropout;
+// Y = RN(RN32(D c X) + R) over [rows, cols] with leading dimensions ldx, ldr,
+// ldy (R may be null); element (i, j) has number first + i * cols + j.
+void launch_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, void* Y, int64_t ldy, int dtype,
+                    int64_t rows, int64_t cols, int64_t first, const Dropout& d, cudaStream_t s);
+
 // All argument checks of qlora_linear_fwd except the workspace (capi.cu).
 int validate_fwd_args(const nf4_weight* w, const void* X, int64_t M, const void* A, const void* B,
                       int r, float alpha, const void* Y, const void* T_save);

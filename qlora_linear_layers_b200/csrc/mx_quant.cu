@@ -1,0 +1,443 @@
+// Microscaled 4-bit floating point: quantise, dequantise, dequantise-transpose.
+//
+// An element is E2M1 (sign, two exponent bits, one mantissa bit: 0, 0.5, 1,
+// 1.5, 2, 3, 4, 6) under a block scale the tensor cores apply themselves:
+//   MXFP4  blocks of 32, scale 2^e (E8M0 byte e + 127):
+//          e = max(floor(log2 amax) - 2, -127)
+//   NVFP4  blocks of 16, scale S (E4M3) under one fp32 scale s per row:
+//          s = 2^k, the smallest (k >= -100) with amax_row <= 6 * 448 * s
+//          S = E4M3(amax_block / s / 6), nearest, ties to even
+//   code = E2M1(x / scale), nearest, ties to even, at most 6 in magnitude.
+// All of it is decided exactly.  x / s and x / 2^e are exact (powers of two).
+// S has a 4-bit significand, so S times the midpoint of two E2M1 values is
+// exact and a quotient x / S that is not on a midpoint differs from it by
+// more than half an fp32 ulp: RN32(x / s / S) rounds to the same code as the
+// real quotient.  A bf16 quotient off a midpoint t is off by at least 2^-8 t,
+// so for bf16 input a product with RN32(1 / S), rounded to a multiple of
+// 2^-14 (one fused multiply-add with 768, one subtraction), decides the same.
+
+#include <algorithm>
+#include <cstdint>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "mx.h"
+
+namespace qnf4 {
+
+// Eight floats -> eight E2M1 codes, element 0 in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(d)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return d;
+}
+
+// Eight E2M1 codes -> four f16x2 words (exact).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t c, uint32_t* h) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(c));
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
+  float2 r;
+  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "r"(h));
+  return r;
+}
+
+// E4M3 byte of a value in [0, 448].
+__device__ __forceinline__ uint32_t to_e4m3(float v) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(0.0f), "f"(v));
+  return d & 0xFFu;
+}
+__device__ __forceinline__ float from_e4m3(uint32_t b) {
+  uint32_t h;
+  const uint16_t p = (uint16_t)b;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(p));
+  return f16x2_to_f32(h).x;
+}
+// 2^(b - 127); byte 0 is the subnormal 2^-127, 255 is NaN.
+__device__ __forceinline__ float from_e8m0(uint32_t b) {
+  return __uint_as_float(b == 0 ? 0x00400000u : b == 255u ? 0x7FFFFFFFu : b << 23);
+}
+
+template <int FMT>
+__device__ __forceinline__ float mx_scale_value(uint32_t b) {
+  return FMT == QLORA_NVFP4 ? from_e4m3(b) : from_e8m0(b);
+}
+
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+// 32 consecutive elements of one row, held as loaded.
+template <typename T> struct Unit;
+template <> struct Unit<__nv_bfloat16> {
+  uint4 w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t word(int j) const {
+    const uint4& v = w[j >> 2];
+    return (j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w;
+  }
+  // fp32 bits of max |x| over elements [16 h, 16 h + 16); NaN and infinities win
+  __device__ __forceinline__ uint32_t amax16(int h) const {
+    __nv_bfloat162 m = __habs2(as2(word(8 * h)));
+#pragma unroll
+    for (int j = 1; j < 8; ++j) m = __hmax2_nan(m, __habs2(as2(word(8 * h + j))));
+    const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+    return max(b << 16, b & 0xFFFF0000u) & 0x7FFFFFFFu;
+  }
+  __device__ __forceinline__ float value(int i) const {
+    return (i & 1) ? bf16_hi(word(i >> 1)) : bf16_lo(word(i >> 1));
+  }
+  __device__ static __forceinline__ __nv_bfloat162 as2(uint32_t v) {
+    return *reinterpret_cast<const __nv_bfloat162*>(&v);
+  }
+};
+template <> struct Unit<float> {
+  float4 w[8];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ float value(int i) const {
+    const float4& v = w[i >> 2];
+    return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+  }
+  __device__ __forceinline__ uint32_t amax16(int h) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(value(16 * h + i)) & 0x7FFFFFFFu);
+    return m;
+  }
+};
+
+// Codes of elements [16 h, 16 h + 16) of a unit under NVFP4's row factor
+// rs = 1 / s and block scale S.
+template <typename T>
+__device__ __forceinline__ uint2 nv_codes16(const Unit<T>& u, int h, float rs, float S) {
+  float v[16];
+  if constexpr (sizeof(T) == 2) {
+    const float m = S == 0.0f ? 0.0f : __frcp_rn(S) * rs;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __fadd_rn(__fmaf_rn(u.value(16 * h + i), m, 768.0f), -768.0f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = S == 0.0f ? 0.0f : __fdiv_rn(__fmul_rn(u.value(16 * h + i), rs), S);
+  }
+  return make_uint2(e2m1x8(v), e2m1x8(v + 8));
+}
+
+template <typename T>
+__device__ __forceinline__ uint2 mx_codes16(const Unit<T>& u, int h, float inv) {
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(u.value(16 * h + i), inv);
+  return make_uint2(e2m1x8(v), e2m1x8(v + 8));
+}
+
+// One CTA a row (rows past the last write the zero scales of the padding).  A
+// thread takes units of 32 elements u = tid + i * blockDim; with KEEP > 0 the
+// row stays in registers (KEEP units a thread) between NVFP4's row maximum
+// and the codes, with KEEP == 0 it is read twice.
+template <typename T, int FMT, int KEEP>
+__global__ void __launch_bounds__(512)
+k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __restrict__ packed,
+              uint8_t* __restrict__ scales, float* __restrict__ row_scale, int* status) {
+  constexpr bool NV = FMT == QLORA_NVFP4;
+  constexpr int kGroup = NV ? 2 : 4;               // units whose scale bytes share a 32-bit word
+  constexpr int kHold = KEEP > 0 ? KEEP : 1;
+  __shared__ uint32_t s_max[16];
+  const int64_t row = blockIdx.x;
+  const int units = K / 32;
+  const int upad = (units + kGroup - 1) / kGroup * kGroup;
+  const int64_t tiles = mx_scale_tiles(FMT, K);
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const int rounds = (upad + nt - 1) / nt;
+  const T* x = X + row * ld;
+  Unit<T> u[kHold];
+  const bool live = row < rows;
+
+  float rs = 1.0f;
+  if constexpr (NV) {
+    uint32_t m = 0;
+    auto take = [&](const Unit<T>& v) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a = v.amax16(h);
+        if (a < kInfBits) m = max(m, a);
+      }
+    };
+    if constexpr (KEEP > 0) {
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i) {
+        const int k = tid + i * nt;
+        if (live && k < units) u[i].load(x + 32 * (int64_t)k);
+        else u[i].zero();
+      }
+#pragma unroll
+      for (int i = 0; i < KEEP; ++i) take(u[i]);
+    } else if (live) {
+      for (int k = tid; k < units; k += nt) {
+        u[0].load(x + 32 * (int64_t)k);
+        take(u[0]);
+      }
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    if (nt > 32) {
+      if ((tid & 31) == 0) s_max[tid >> 5] = m;
+      __syncthreads();
+      m = __reduce_max_sync(0xFFFFFFFFu, (tid & 31) < (nt >> 5) ? s_max[tid & 31] : 0u);
+    }
+    // s = 2^(f - 127): amax = 1.m 2^E <= 2688 s = 1.3125 * 2^11 s
+    uint32_t f = 127;
+    if (m) f = (uint32_t)max((int)(m >> 23) - 11 + ((m & 0x7FFFFFu) > 0x280000u ? 1 : 0), 27);
+    rs = __uint_as_float((254u - f) << 23);
+    if (live && tid == 0) row_scale[row] = __uint_as_float(f << 23);
+  }
+
+  for (int i = 0; i < rounds; ++i) {
+    const int k = tid + i * nt;
+    const bool in = live && k < units;
+    Unit<T>* v = &u[0];
+    if constexpr (!NV || KEEP == 0) {
+      if (in) u[0].load(x + 32 * (int64_t)k);
+      else u[0].zero();
+    }
+    uint32_t sb = 0;                               // this unit's scale bytes, in their place of the word
+    uint4 codes;
+    bool bad = false;
+    auto body = [&](const Unit<T>& w) {
+      if constexpr (NV) {
+        uint2 c[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t a = w.amax16(h);
+          const bool nf = a >= kInfBits;
+          const uint32_t code = to_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(a), rs), 6.0f));
+          c[h] = nv_codes16(w, h, rs, from_e4m3(code));
+          if (nf) c[h] = make_uint2(0, 0);
+          bad |= nf;
+          sb |= (nf ? 0x7Fu : code) << (8 * (2 * (k & 1) + h));
+        }
+        codes = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+      } else {
+        const uint32_t a = max(w.amax16(0), w.amax16(1));
+        const bool nf = a >= kInfBits;
+        const uint32_t code = (uint32_t)max((int)(a >> 23) - 2, 0);
+        const float inv = __uint_as_float((254u - code) << 23);
+        const uint2 c0 = mx_codes16(w, 0, inv), c1 = mx_codes16(w, 1, inv);
+        codes = nf ? make_uint4(0, 0, 0, 0) : make_uint4(c0.x, c0.y, c1.x, c1.y);
+        bad |= nf;
+        sb |= (nf ? 0xFFu : code) << (8 * (k & 3));
+      }
+    };
+    if constexpr (NV && KEEP > 0) {
+#pragma unroll
+      for (int j = 0; j < KEEP; ++j)
+        if (j == i) body(u[j]);
+      (void)v;
+    } else {
+      body(u[0]);
+    }
+    if (!in) sb = 0;
+    sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 1);
+    if (!NV) sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
+    if (in) {
+      *reinterpret_cast<uint4*>(packed + row * (K / 2) + 16 * (int64_t)k) = codes;
+      if (bad) set_status(status, QLORA_ERR_NONFINITE);
+    }
+    if (k < upad && (k & (kGroup - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(row, (NV ? 2 : 1) * (int64_t)k, tiles)) = sb;
+  }
+}
+
+template <typename T, int FMT>
+static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int64_t ld, uint8_t* packed,
+                                 uint8_t* scales, float* row_scale, int* status, cudaStream_t s) {
+  const int units = (int)(cols / 32);
+  const int upad = FMT == QLORA_NVFP4 ? (units + 1) / 2 * 2 : (units + 3) / 4 * 4;
+  const int64_t prow = (rows + 127) / 128 * 128;
+  auto run = [&](auto kern, int per) {
+    const int nt = std::min(512, std::max(32, ((upad + per - 1) / per + 31) / 32 * 32));
+    kern<<<(unsigned)prow, nt, 0, s>>>((const T*)X, ld, (int)rows, (int)cols, packed, scales, row_scale, status);
+  };
+  constexpr bool big = sizeof(T) == 4;
+  if (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);
+  else if (upad <= 256) run(k_mx_quantize<T, FMT, 1>, 1);
+  else if (upad <= 1024) run(k_mx_quantize<T, FMT, 2>, 2);
+  else if (!big && upad <= 2048) run(k_mx_quantize<T, FMT, big ? 2 : 4>, 4);
+  else run(k_mx_quantize<T, FMT, 0>, 1);
+}
+
+void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
+                        uint8_t* packed, uint8_t* scales, float* row_scale, int* status,
+                        cudaStream_t s) {
+  if (dtype == QLORA_F32) {
+    if (format == QLORA_NVFP4) launch_mx_quantize_t<float, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+    else launch_mx_quantize_t<float, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+  } else {
+    if (format == QLORA_NVFP4) launch_mx_quantize_t<__nv_bfloat16, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+    else launch_mx_quantize_t<__nv_bfloat16, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+  }
+}
+
+// ===========================================================================
+// Dequantise: value = RNbf16(RN32(q S s)).  q S is exact (2 + 4 significant
+// bits), and so is the bf16 result when s is a power of two, as the quantiser
+// writes it.  Eight elements a thread and step: a 4-byte code word, a 16-byte
+// store.  blockDim.x threads share a row, blockDim.y rows a CTA.
+// ===========================================================================
+template <int FMT>
+__device__ __forceinline__ uint4 mx_values8(uint32_t c, float S, float rs) {
+  uint32_t h[4], o[4];
+  e2m1x8_to_f16(c, h);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = f16x2_to_f32(h[j]);
+    float a = __fmul_rn(f.x, S), b = __fmul_rn(f.y, S);
+    if (FMT == QLORA_NVFP4) { a = __fmul_rn(a, rs); b = __fmul_rn(b, rs); }
+    o[j] = pack_bf16x2(a, b);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <int FMT>
+__global__ void __launch_bounds__(256)
+k_mx_dequantize(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales,
+                const float* __restrict__ row_scale, int rows, int K, __nv_bfloat16* __restrict__ out) {
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= rows) return;
+  const int64_t tiles = mx_scale_tiles(FMT, K);
+  const float rs = FMT == QLORA_NVFP4 ? row_scale[row] : 1.0f;
+  const uint32_t* c = reinterpret_cast<const uint32_t*>(packed + row * (K / 2));
+  uint4* o = reinterpret_cast<uint4*>(out + row * K);
+  const uint8_t* sc = scales + mx_scale_offset(row, 0, tiles);
+  const int words = K / 8;
+#pragma unroll 4
+  for (int w = threadIdx.x; w < words; w += blockDim.x) {
+    const int col = w / (mx_block(FMT) / 8);
+    __stcs(o + w, mx_values8<FMT>(__ldg(c + w), mx_scale_value<FMT>(__ldg(sc + (int64_t)(col >> 2) * 512 + (col & 3))), rs));
+  }
+}
+
+void launch_mx_dequantize(const qlora_mx_tensor* t, void* out, cudaStream_t s) {
+  int tx = 8;
+  while (tx < 256 && tx < t->cols / 8) tx *= 2;
+  const dim3 block(tx, 256 / tx);
+  const unsigned grid = (unsigned)((t->rows + block.y - 1) / block.y);
+  auto run = [&](auto kern) {
+    kern<<<grid, block, 0, s>>>(t->packed, t->scales, t->row_scale, (int)t->rows, (int)t->cols, (__nv_bfloat16*)out);
+  };
+  if (t->format == QLORA_NVFP4) run(k_mx_dequantize<QLORA_NVFP4>);
+  else run(k_mx_dequantize<QLORA_MXFP4>);
+}
+
+// ===========================================================================
+// Dequantise-transpose for the backward's dX: CTA tile 64 rows (n) x 128
+// columns (k).  Thread (pr, qk) expands rows 2 pr, 2 pr + 1, columns
+// [16 qk, 16 qk + 16) -- within one block of either format -- and stores each
+// column's pair of rows as one word of the transposed tile in shared memory (a
+// warp's words are consecutive); the tile leaves in 16-byte stores.
+// ===========================================================================
+template <int FMT>
+__global__ void __launch_bounds__(256)
+k_mx_dequant_t(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales,
+               const float* __restrict__ row_scale, int N, int K, __nv_bfloat16* __restrict__ Wt) {
+  constexpr int kPitch = 36;                       // words per transposed row (32 + pad, 16-byte rows)
+  __shared__ __align__(16) uint32_t tileT[128 * kPitch];
+  const int n0 = blockIdx.y * 64, k0 = blockIdx.x * 128;
+  const int tid = threadIdx.x;
+  const int pr = tid & 31, qk = tid >> 5;
+  const int k = k0 + 16 * qk;
+  const int64_t tiles = mx_scale_tiles(FMT, K);
+  uint32_t v[2][8];                                // bf16 pairs of the two rows
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int n = n0 + 2 * pr + h;
+    uint4 a = make_uint4(0, 0, 0, 0), b = a;
+    if (k < K && n < N) {
+      const uint2 cw = *reinterpret_cast<const uint2*>(packed + ((int64_t)n * K + k) / 2);
+      const float S = mx_scale_value<FMT>(scales[mx_scale_offset(n, k / mx_block(FMT), tiles)]);
+      const float rs = FMT == QLORA_NVFP4 ? row_scale[n] : 1.0f;
+      a = mx_values8<FMT>(cw.x, S, rs);
+      b = mx_values8<FMT>(cw.y, S, rs);
+    }
+    v[h][0] = a.x; v[h][1] = a.y; v[h][2] = a.z; v[h][3] = a.w;
+    v[h][4] = b.x; v[h][5] = b.y; v[h][6] = b.z; v[h][7] = b.w;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    tileT[(16 * qk + 2 * j) * kPitch + pr] = prmt(v[0][j], v[1][j], 0x5410);
+    tileT[(16 * qk + 2 * j + 1) * kPitch + pr] = prmt(v[0][j], v[1][j], 0x7632);
+  }
+  __syncthreads();
+  for (int i = tid; i < 128 * 8; i += 256) {
+    const int kr = i >> 3, ch = i & 7;             // transposed row, 16-byte chunk (8 columns n)
+    const int kk = k0 + kr, nn = n0 + ch * 8;
+    if (kk < K && nn < N)                          // N % 8 == 0: a chunk is whole
+      *reinterpret_cast<uint4*>(Wt + (int64_t)kk * N + nn) =
+          *reinterpret_cast<const uint4*>(&tileT[kr * kPitch + ch * 4]);
+  }
+}
+
+void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s) {
+  const dim3 grid((unsigned)((w->cols + 127) / 128), (unsigned)((w->rows + 63) / 64));
+  auto run = [&](auto kern) {
+    kern<<<grid, 256, 0, s>>>(w->packed, w->scales, w->row_scale, (int)w->rows, (int)w->cols, (__nv_bfloat16*)Wt);
+  };
+  if (w->format == QLORA_NVFP4) run(k_mx_dequant_t<QLORA_NVFP4>);
+  else run(k_mx_dequant_t<QLORA_MXFP4>);
+}
+
+// ===========================================================================
+// Adapter factors for the product: zero-padded to RP columns and, for NVFP4,
+// divided by the row scale that the product's epilogue multiplies back.  The
+// quantiser's row scales are powers of two, for which this is exact; any
+// other row scale costs one more bf16 rounding of the factor.
+// ===========================================================================
+__global__ void k_mx_pad_rows(const __nv_bfloat16* in, int64_t rows, int r, int ldi, int RP,
+                              const float* __restrict__ row_scale, __nv_bfloat16* out) {
+  const int64_t total = rows * RP;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / RP;
+    const int c = (int)(i % RP);
+    float v = c < r ? __bfloat162float(in[row * ldi + c]) : 0.0f;
+    if (row_scale) v = __fdiv_rn(v, row_scale[row]);
+    out[i] = __float2bfloat16_rn(v);
+  }
+}
+
+void launch_mx_pad_rows(const void* in, int64_t rows, int r, int ldi, int RP, const float* row_scale,
+                        void* out, cudaStream_t s) {
+  const int grid = (int)std::min<int64_t>((rows * RP + 255) / 256, 148 * 8);
+  k_mx_pad_rows<<<grid, 256, 0, s>>>((const __nv_bfloat16*)in, rows, r, ldi, RP, row_scale, (__nv_bfloat16*)out);
+}
+
+}  // namespace qnf4
