@@ -31,24 +31,12 @@
 #include "common.cuh"
 #include "gemm.h"
 #include "mx.h"
+#include "mx_gemm.cuh"
 
 namespace qnf4 {
 namespace mx {
 
-constexpr int BW = 128;                            // weight rows of a tile (MMA M)
-constexpr int BKB = 128;                           // bytes of a row and stage: 256 codes or 64 bf16
 constexpr int NUM_THREADS = 192;
-
-struct Args {
-  const uint8_t* xs;        // token scale tiles
-  const uint8_t* ws;        // weight scale tiles
-  const float* xr;          // row scales (NVFP4)
-  const float* wr;
-  __nv_bfloat16* out;
-  int M, N, K;
-  int na;                   // adapter K steps
-  int* status;
-};
 
 template <int FMT, int BN>
 struct Shape {
@@ -80,63 +68,12 @@ struct Smem {
 template <int FMT, int BN>
 constexpr size_t smem_bytes() { return sizeof(Smem<FMT, BN>) + 1024; }
 
-// 512-byte scale tile in shared memory: 32 rows of 16 bytes, no swizzle,
-// groups of eight rows 128 bytes apart.
-__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(128u >> 4) << 16;
-  d |= (uint64_t)(128u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  return d;
-}
-
-__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
-}
-
-// Instruction descriptor of the 4-bit block-scaled kinds: A = B = E2M1, both
-// K-major, K = 64; sf is the byte of a scale word where this K step begins
-// (0, or 2 in the second half of an MXFP4 word).
-template <int FMT>
-__host__ __device__ constexpr uint32_t idesc_mx(int N, uint32_t sf) {
-  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
-         ((FMT == QLORA_MXFP4 ? 1u : 0u) << 23) | (1u << 27) | (sf << 29);
-}
-
-template <int FMT>
-__device__ __forceinline__ void mma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                       uint32_t sfb, uint32_t accumulate) {
-  if constexpr (FMT == QLORA_NVFP4)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
-        :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
-}
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-      :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
-}
-
-// Bounded wait for a copy in flight after the kernel has given up (the abort
-// flag is set and no longer looked at).
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const int* st) {
-  const uint64_t t0 = globaltimer_ns(), lim = wait_limit_ns(st);
-  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < lim) {
-  }
-}
-
 template <int FMT, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
           const __grid_constant__ CUtensorMap tm_x,       // [M, K / 2] bytes
+          const __grid_constant__ CUtensorMap tm_sw,      // scale tiles of w
+          const __grid_constant__ CUtensorMap tm_sx,      // scale tiles of x
           const __grid_constant__ CUtensorMap tm_wad,     // [N, RP] bf16
           const __grid_constant__ CUtensorMap tm_xad,     // [M, RP] bf16
           const Args p) {
@@ -175,12 +112,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   volatile int* abort = &S.abort;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const int64_t tiles = mx_scale_tiles(FMT, p.K);
-      const int rb0 = m0 / 128, rb_all = (p.M + 127) / 128;
-      const uint8_t* sw = p.ws + (int64_t)(n0 / 128) * tiles * 512;
-      const uint8_t* sx = p.xs + (int64_t)rb0 * tiles * 512;
-      const int nrb = min(RB, rb_all - rb0);
+    if (elect_one()) {
       int i = 0;
       for (; i < nsteps; ++i) {
         const int s = i % NS;
@@ -191,20 +123,18 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
           tma_load_2d(S.x[s], &tm_xad, &S.full[s], i * 64, m0);
         } else {
           const int ks = i - p.na;
-          const int nt = (int)min((int64_t)NT, tiles - (int64_t)ks * NT);
-          mbar_arrive_expect_tx(&S.full[s], Sh::W_BYTES + Sh::X_BYTES + (1 + nrb) * nt * 512);
+          mbar_arrive_expect_tx(&S.full[s], Sh::STAGE);
           tma_load_2d(S.w[s], &tm_w, &S.full[s], ks * BKB, n0);
           tma_load_2d(S.x[s], &tm_x, &S.full[s], ks * BKB, m0);
-          bulk_load(S.sw[s], sw + (int64_t)ks * NT * 512, nt * 512, &S.full[s]);
-          for (int b = 0; b < nrb; ++b)
-            bulk_load(S.sx[s] + b * NT * 512, sx + ((int64_t)b * tiles + (int64_t)ks * NT) * 512, nt * 512, &S.full[s]);
+          tma_load_3d(S.sw[s], &tm_sw, &S.full[s], 0, ks * NT, n0 / 128);
+          tma_load_3d(S.sx[s], &tm_sx, &S.full[s], 0, ks * NT, m0 / 128);
         }
       }
       if (i < nsteps || *abort)                                   // a wait gave up: let the copies in flight land
         for (int j = max(0, i - NS); j < i; ++j) drain_wait(&S.full[j % NS], (j / NS) & 1, p.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kId16 = idesc_bf16_f32(BW, BN);
       const uint32_t sf0 = tmem + Sh::D_COLS;
       const uint32_t sub = (uint32_t)(m0 % 128) / 32;            // token tile's place in its scale block
@@ -246,7 +176,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
         for (int q = 0; q < nq; ++q) {
           const int t = NV ? q : q >> 1;
           const uint32_t sf = NV ? 0u : 2u * (q & 1);
-          mma_mx<FMT>(tmem, a + 2 * q, b + 2 * q, idesc_mx<FMT>(BN, sf), sfw + 4 * t, sfx + 4 * RB * t + sub,
+          mma_mx<FMT>(tmem, a + 2 * q, b + 2 * q, idesc_mx<FMT>(BW, BN, sf), sfw + 4 * t, sfx + 4 * RB * t + sub,
                       (i > 0 || q > 0) ? 1u : 0u);
         }
         mma_commit(&S.empty[s]);
@@ -280,25 +210,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
           for (int j = 0; j < 16; ++j)
             v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(S.rx[c + j], rw)));
         }
-        if (pairs) {
-          // lanes (2i, 2i + 1) swap halves: even lanes store token c + j, odd
-          // lanes token c + j + 1, both the outputs of the even lane's column
-          const int col = n - (odd ? 1 : 0);
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const uint32_t mine = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
-            const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
-            const uint32_t o = odd ? prmt(other, mine, 0x7632) : prmt(mine, other, 0x5410);
-            const int m = m0 + c + j + (odd ? 1 : 0);
-            if (m < p.M && col < p.N)
-              *reinterpret_cast<uint32_t*>(p.out + (int64_t)m * p.N + col) = o;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (m0 + c + j < p.M && n < p.N)
-              p.out[(int64_t)(m0 + c + j) * p.N + n] = __float2bfloat16_rn(__uint_as_float(v[j]));
-        }
+        store_columns<16>(p, v, m0 + c, n, n - (odd ? 1 : 0), odd, pairs);
       }
     }
   }
@@ -313,10 +225,14 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
 template <int FMT, int BN>
 static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
                   int RP, const Args& a, cudaStream_t s) {
-  CUtensorMap tw, tx, twa, txa;
+  CUtensorMap tw, tx, tsw, tsx, twa, txa;
   const uint64_t kb = (uint64_t)a.K / 2;
   if (!make_tmap_2d_u8(&tw, w->packed, kb, a.N, kb, BKB, BW, true)) return QLORA_ERR_CUDA;
   if (!make_tmap_2d_u8(&tx, x->packed, kb, a.M, kb, BKB, BN, true)) return QLORA_ERR_CUDA;
+  using Sh = Shape<FMT, BN>;
+  if (!make_scale_tmap(&tsw, w->scales, FMT, a.N, a.K, Sh::NT, 1) ||
+      !make_scale_tmap(&tsx, x->scales, FMT, a.M, a.K, Sh::NT, Sh::RB))
+    return QLORA_ERR_CUDA;
   twa = tw;
   txa = tx;
   if (RP) {
@@ -328,7 +244,7 @@ static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   set_smem_attr_once(k_mx_gemm<FMT, BN>, (int)bytes, attr_devs);
   const dim3 grid((a.N + BW - 1) / BW, (a.M + BN - 1) / BN);
-  k_mx_gemm<FMT, BN><<<grid, NUM_THREADS, bytes, s>>>(tw, tx, twa, txa, a);
+  k_mx_gemm<FMT, BN><<<grid, NUM_THREADS, bytes, s>>>(tw, tx, tsw, tsx, twa, txa, a);
   return QLORA_OK;
 }
 
@@ -338,22 +254,20 @@ static int launch_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const 
   if (a.M <= 16) return launch<FMT, 16>(x, w, tokad, wad, RP, a, s);
   if (a.M <= 32) return launch<FMT, 32>(x, w, tokad, wad, RP, a, s);
   if (a.M <= 64) return launch<FMT, 64>(x, w, tokad, wad, RP, a, s);
-  if (a.M <= 128) return launch<FMT, 128>(x, w, tokad, wad, RP, a, s);
-  return launch<FMT, 256>(x, w, tokad, wad, RP, a, s);
+  return launch<FMT, 128>(x, w, tokad, wad, RP, a, s);
 }
 
 }  // namespace mx
 
 int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad,
                    const void* wad, int RP, void* Y, int* status, cudaStream_t s, int num_sms) {
-  (void)num_sms;
   mx::Args a{};
-  a.xs = x->scales; a.ws = w->scales;
   a.xr = x->row_scale; a.wr = w->row_scale;
   a.out = static_cast<__nv_bfloat16*>(Y);
   a.M = (int)x->rows; a.N = (int)w->rows; a.K = (int)x->cols;
   a.na = RP / 64;
   a.status = status;
+  if (a.M > 128) return mx::launch_gemm_pair(x, w, tokad, wad, RP, a, s, num_sms);
   return x->format == QLORA_NVFP4 ? mx::launch_fmt<QLORA_NVFP4>(x, w, tokad, wad, RP, a, s)
                                   : mx::launch_fmt<QLORA_MXFP4>(x, w, tokad, wad, RP, a, s);
 }

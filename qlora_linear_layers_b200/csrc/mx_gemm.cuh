@@ -1,0 +1,163 @@
+// Pieces that the kernels of the microscaled product share.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "gemm.h"
+#include "mx.h"
+
+namespace qnf4 {
+namespace mx {
+
+constexpr int BW = 128;                            // weight rows of a CTA's tile
+constexpr int BKB = 128;                           // bytes of a row and stage: 256 codes or 64 bf16
+
+struct Args {
+  const float* xr;          // row scales (NVFP4)
+  const float* wr;
+  __nv_bfloat16* out;
+  int M, N, K;
+  int na;                   // adapter K steps
+  int* status;
+};
+
+int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
+                     int RP, const Args& a, cudaStream_t s, int num_sms);
+
+// True in one lane of a converged warp.  The tensor-core and TMA instructions
+// take their operands from uniform registers; behind an elect.sync the compiler
+// knows that one lane is active and issues them directly, behind a comparison of
+// the lane number it loops over the lanes (measured: 154 against 45 cycles of
+// issue for an MMA, 73 against 32 for a scale copy).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+// Tensor map of a scale array: 512-byte tiles, tiles along K, 128-row blocks;
+// boxes of nt x rb tiles.  Tiles past the array read as zero.
+inline bool make_scale_tmap(CUtensorMap* tm, const uint8_t* scales, int format, int64_t rows, int64_t cols,
+                            uint32_t nt, uint32_t rb) {
+  const uint64_t tiles = (uint64_t)mx_scale_tiles(format, cols);
+  const uint64_t dims[3] = {256, tiles, (uint64_t)((rows + 127) / 128)};
+  const uint64_t strides[2] = {512, tiles * 512};
+  const uint32_t box[3] = {256, nt, rb};
+  return make_tmap_3d(tm, scales, true, dims, strides, box, false);
+}
+
+// 512-byte scale tile in shared memory: 32 rows of 16 bytes, no swizzle,
+// groups of eight rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(128u >> 4) << 16;
+  d |= (uint64_t)(128u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  return d;
+}
+
+// Scale tile -> four tensor-memory columns, replicated to the four lane groups.
+__device__ __forceinline__ void scale_copy(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void scale_copy_pair(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" :: "r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of the 4-bit block-scaled kinds: A = B = E2M1, both
+// K-major, K = 64; sf is the byte of a scale word where this K step begins
+// (0, or 2 in the second half of an MXFP4 word).
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) |
+         ((FMT == QLORA_MXFP4 ? 1u : 0u) << 23) | ((uint32_t)(M >> 7) << 27) | (sf << 29);
+}
+
+#define QNF4_MMA_MX(NAME, GROUP)                                                                             \
+  template <int FMT>                                                                                         \
+  __device__ __forceinline__ void NAME(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,     \
+                                       uint32_t sfb, uint32_t accumulate) {                                  \
+    if constexpr (FMT == QLORA_NVFP4)                                                                        \
+      asm volatile(                                                                                          \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                  \
+          "tcgen05.mma." GROUP ".kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" \
+          :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");            \
+    else                                                                                                     \
+      asm volatile(                                                                                          \
+          "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"                                                  \
+          "tcgen05.mma." GROUP ".kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" \
+          :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");            \
+  }
+QNF4_MMA_MX(mma_mx, "cta_group::1")
+QNF4_MMA_MX(mma_mx_pair, "cta_group::2")
+#undef QNF4_MMA_MX
+
+// Warp-wide: thread t reads 32 consecutive 32-bit columns of its lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Tiled 3-D load into this CTA's shared memory whose completion is counted on
+// an mbarrier of either CTA of the pair (no multicast).
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tmap, uint32_t mbar_cluster,
+                                                 int32_t c0, int32_t c1, int32_t c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"(smem_u32(smem_dst)), "l"(tmap), "r"(mbar_cluster), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Bounded wait for a copy in flight after the kernel has given up (the abort
+// flag is set and no longer looked at).
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const int* st) {
+  const uint64_t t0 = globaltimer_ns(), lim = wait_limit_ns(st);
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < lim) {
+  }
+}
+
+// A lane's NC results (tokens m .. m + NC - 1 of output column n) -> bf16 rows.
+// With an even N lanes (2i, 2i + 1) swap halves: even lanes store tokens m + j,
+// odd lanes m + j + 1, both the two outputs at `col`, the even lane's column.
+template <int NC>
+__device__ __forceinline__ void store_columns(const Args& p, const uint32_t* v, int m, int n, int col, bool odd,
+                                              bool pairs) {
+  if (pairs) {
+    const int first = m + (odd ? 1 : 0);
+    const int left = col < p.N ? p.M - first : 0;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (int64_t)first * p.N + col);
+#pragma unroll
+    for (int j = 0; j < NC; j += 2) {
+      const uint32_t mine = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+      const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, mine, 1);
+      const uint32_t o = odd ? prmt(other, mine, 0x7632) : prmt(mine, other, 0x5410);
+      if (j < left) *dst = o;
+      dst += p.N;                                  // two bf16 rows = N words
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      if (m + j < p.M && n < p.N) p.out[(int64_t)(m + j) * p.N + n] = __float2bfloat16_rn(__uint_as_float(v[j]));
+  }
+}
+
+}  // namespace mx
+}  // namespace qnf4

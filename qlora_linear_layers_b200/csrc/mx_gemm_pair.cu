@@ -1,0 +1,327 @@
+// Large products of two microscaled 4-bit matrices: pairs of SMs
+// (tcgen05 cta_group::2), persistent.
+//
+//   Y^T tile = 256 weight rows x PN tokens; CTA r of a pair owns weight rows
+//   128 r .. 128 r + 127 of the tile in its tensor memory and loads those rows
+//   and PN / 2 of the tokens, so a stage (256 elements of K) brings half the
+//   token codes to each SM.
+//
+// The tensor core is the bound.  Measured on B200, one MMA (256 x PN x 64)
+// takes 45 + PN / 2 cycles whatever its kind and operands, so a tile is as wide
+// as the rounds of tiles allow (up to 256 tokens), and the issuing thread has
+// to keep up with it:
+//  * a stage's 3 NT scale copies and 4 MMAs leave one thread in about 570
+//    cycles (NVFP4) against 694 of MMA time; nothing else is in its loop;
+//  * each pipeline stage has scale columns of its own in tensor memory (PN <=
+//    256 accumulator columns leave 256, five stages of 48), so the "full"
+//    barrier, which implies that the stage's last readers are done, is the only
+//    wait of a stage;
+//  * one accumulator: eight epilogue warps take it to registers as it is (128
+//    values a thread), hand it back, and scale, round and store under the next
+//    tile's MMAs.  Two accumulators would hide that read too, but with tiles of
+//    192 tokens, whose MMAs do 8 % less per cycle.
+// The adapter's bf16 K steps (kind::f16) come first and are complete before the
+// block-scaled MMAs of the tile begin: MMAs of two kinds need not run in order.
+//
+// Every scale tile comes with the stage: each CTA loads the scales of its own
+// 128 weight rows and of all PN tokens (one or two 128-row blocks), and the
+// even CTA's tcgen05.cp moves both CTAs' copies to their tensor memories.
+// Every wait is bounded (QLORA_ERR_TIMEOUT).
+
+#include <algorithm>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "gemm.h"
+#include "mx.h"
+#include "mx_gemm.cuh"
+
+namespace qnf4 {
+namespace mx {
+
+constexpr int P_EPI = 8;                           // epilogue warps
+constexpr int P_THREADS = 64 + 32 * P_EPI;         // warp 0 TMA, 1 MMA, 2-9 epilogue
+constexpr uint16_t kBoth = 0x3;
+
+template <int FMT, int PN>
+struct PairShape {
+  static_assert(PN % 64 == 0 && PN <= 256, "token tile");
+  static constexpr int PNH = PN / 2;                              // tokens each CTA loads
+  static constexpr int NT = FMT == QLORA_NVFP4 ? 4 : 2;           // scale tiles of 256 elements
+  static constexpr int RB = PN == 128 ? 1 : 2;                    // 128-row scale blocks of the tokens
+  static constexpr int W_BYTES = BW * BKB, X_BYTES = PNH * BKB;
+  static constexpr int SW_BYTES = NT * 512, SX_BYTES = RB * NT * 512;
+  static constexpr int NS = 5;
+  static constexpr int SF_COLS = 4 * NT * (1 + RB);               // a stage's scale columns
+  static_assert(PN + NS * SF_COLS <= 512, "tensor memory columns");
+};
+
+template <int FMT, int PN>
+struct PairSmem {
+  using Sh = PairShape<FMT, PN>;
+  uint8_t w[Sh::NS][Sh::W_BYTES];
+  uint8_t x[Sh::NS][Sh::X_BYTES];
+  uint8_t sw[Sh::NS][Sh::SW_BYTES];
+  uint8_t sx[Sh::NS][Sh::SX_BYTES];
+  float rx[2][PN];
+  uint64_t full[Sh::NS], empty[Sh::NS], acc_full, acc_empty, kind, done;
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int FMT, int PN>
+__global__ void __launch_bounds__(P_THREADS, 1)
+k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+               const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_sx,
+               const __grid_constant__ CUtensorMap tm_wad, const __grid_constant__ CUtensorMap tm_xad,
+               const Args p) {
+  using Sh = PairShape<FMT, PN>;
+  constexpr int NS = Sh::NS, NT = Sh::NT, RB = Sh::RB, PNH = Sh::PNH;
+  constexpr bool NV = FMT == QLORA_NVFP4;
+  extern __shared__ uint8_t smem_raw[];
+  PairSmem<FMT, PN>& S =
+      *reinterpret_cast<PairSmem<FMT, PN>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int tiles_n = (p.N + 2 * BW - 1) / (2 * BW);
+  const int n_tiles = tiles_n * ((p.M + PN - 1) / PN);
+  const int cluster = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const int nk = (p.K + 255) / 256;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&S.full[i], 1);                    // leader's expect_tx; bytes of both CTAs
+      mbar_init(&S.empty[i], 1);                   // multicast commit
+    }
+    mbar_init(&S.acc_full, 1);                     // multicast commit
+    mbar_init(&S.acc_empty, 2 * P_EPI);            // epilogue warps of both CTAs
+    mbar_init(&S.kind, 1);
+    mbar_init(&S.done, 1);
+    S.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&S.tmem_base, 512);
+    tmem_relinquish_pair();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_sw);
+    tma_prefetch_desc(&tm_sx);
+  }
+  tc_fence_before();
+  cluster_sync();                                  // barriers of both CTAs initialised
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  volatile int* abort = &S.abort;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int tile = cluster; tile < n_tiles && ok; tile += n_clusters) {
+        const int n0 = (tile % tiles_n) * (2 * BW) + (int)rank * BW;
+        const int mt = (tile / tiles_n) * PN, m0 = mt + (int)rank * PNH;
+        for (int i = -p.na; i < nk; ++i) {
+          if (!(ok = mbar_wait_cluster(&S.empty[s], ph ^ 1, abort, p.status))) break;
+          const uint32_t full0 = mapa_shared(smem_u32(&S.full[s]), 0);
+          if (i < 0) {
+            const int c = (i + p.na) * 64;
+            if (leader) mbar_arrive_expect_tx(&S.full[s], 2 * (Sh::W_BYTES + Sh::X_BYTES));
+            tma_load_2d_pair(S.w[s], &tm_wad, full0, c, n0);
+            tma_load_2d_pair(S.x[s], &tm_xad, full0, c, m0);
+          } else {
+            if (leader)
+              mbar_arrive_expect_tx(&S.full[s], 2 * (Sh::W_BYTES + Sh::X_BYTES + Sh::SW_BYTES + Sh::SX_BYTES));
+            tma_load_2d_pair(S.w[s], &tm_w, full0, i * BKB, n0);
+            tma_load_2d_pair(S.x[s], &tm_x, full0, i * BKB, m0);
+            tma_load_3d_pair(S.sw[s], &tm_sw, full0, 0, i * NT, n0 / 128);
+            tma_load_3d_pair(S.sx[s], &tm_sx, full0, 0, i * NT, mt / 128);
+          }
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (leader && elect_one()) {
+      constexpr uint32_t kId16 = idesc_bf16_f32(2 * BW, PN);
+      const uint64_t a0 = sw128_kmajor_desc(smem_u32(S.w[0])), b0 = sw128_kmajor_desc(smem_u32(S.x[0]));
+      const uint64_t sw0 = scale_desc(smem_u32(S.sw[0])), sx0 = scale_desc(smem_u32(S.sx[0]));
+      int s = 0;
+      uint32_t ph = 0, tp = 0;                     // stage, its phase; the tile's phase
+      bool ok = true;
+      for (int tile = cluster; tile < n_tiles && ok; tile += n_clusters, tp ^= 1) {
+        const uint32_t sub = (uint32_t)((tile / tiles_n) * PN % 128) / 32;
+        ok = mbar_wait_cluster(&S.acc_empty, tp ^ 1, abort, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < p.na; ++i) {
+          if (!(ok = mbar_wait_cluster(&S.full[s], ph, abort, p.status))) break;
+          tc_fence_after();
+          const uint64_t a = a0 + (uint32_t)(s * (Sh::W_BYTES / 16)), b = b0 + (uint32_t)(s * (Sh::X_BYTES / 16));
+#pragma unroll
+          for (int q = 0; q < 4; ++q) mma_ss_pair(tmem, a + 2 * q, b + 2 * q, kId16, (i > 0 || q > 0) ? 1u : 0u);
+          mma_commit_pair_mc(&S.empty[s], kBoth);
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+        if (ok && p.na > 0) {                      // the adapter's MMAs are complete
+          mma_commit_pair_mc(&S.kind, 0x1);
+          ok = mbar_wait_cluster(&S.kind, tp, abort, p.status);
+          tc_fence_after();
+        }
+        if (!ok) break;
+        for (int i = 0; i < nk; ++i) {
+          if (!(ok = mbar_wait_cluster(&S.full[s], ph, abort, p.status))) break;
+          tc_fence_after();
+          const uint64_t a = a0 + (uint32_t)(s * (Sh::W_BYTES / 16)), b = b0 + (uint32_t)(s * (Sh::X_BYTES / 16));
+          const uint64_t sw = sw0 + (uint32_t)(s * (Sh::SW_BYTES / 16)), sx = sx0 + (uint32_t)(s * (Sh::SX_BYTES / 16));
+          const uint32_t sfw = tmem + PN + s * Sh::SF_COLS, sfx = sfw + 4 * NT;
+          const int nq = min(4, (p.K - i * 256 + 63) / 64);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int c = NV ? q : q >> 1;         // scale tile of this K step
+            if (q >= nq) break;
+            if (NV || !(q & 1)) {
+              scale_copy_pair(sfw + 4 * c, sw + 32 * c);
+#pragma unroll
+              for (int r = 0; r < RB; ++r) scale_copy_pair(sfx + 4 * (RB * c + r), sx + 32 * (r * NT + c));
+            }
+            mma_mx_pair<FMT>(tmem, a + 2 * q, b + 2 * q, idesc_mx<FMT>(2 * BW, PN, NV ? 0u : 2u * (q & 1)),
+                             sfw + 4 * c, sfx + 4 * RB * c + sub, (i > 0 || q > 0 || p.na > 0) ? 1u : 0u);
+          }
+          mma_commit_pair_mc(&S.empty[s], kBoth);
+          if (++s == NS) { s = 0; ph ^= 1; }
+        }
+        if (ok) mma_commit_pair_mc(&S.acc_full, kBoth);
+      }
+      mma_commit_pair_mc(&S.done, 0x1);            // every MMA has read its operands
+      mbar_wait(&S.done, 0, abort, p.status);
+    }
+  } else {
+    // warps (2 + e): lane quadrant warp % 4, column half e / 4
+    constexpr int HC = PN / 2;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + half * HC;
+    const bool odd = lane & 1;
+    const bool pairs = (p.N & 1) == 0;
+    const uint32_t acc_empty0 = mapa_shared(smem_u32(&S.acc_empty), 0);
+    uint32_t tp = 0;
+    for (int tile = cluster; tile < n_tiles; tile += n_clusters, tp ^= 1) {
+      const int n = (tile % tiles_n) * (2 * BW) + (int)rank * BW + quad * 32 + lane;
+      const int mt = (tile / tiles_n) * PN, m0 = mt + half * HC;
+      float rw = 1.0f;
+      if (NV) {
+        if (n < p.N) rw = p.wr[n];
+        // the readers of this buffer, two tiles ago, passed the last tile's barrier
+        for (int i = threadIdx.x - 64; i < PN; i += 32 * P_EPI) S.rx[tp][i] = mt + i < p.M ? p.xr[mt + i] : 0.0f;
+        asm volatile("bar.sync 1, %0;" :: "n"(32 * P_EPI) : "memory");
+      }
+      if (!mbar_wait_cluster(&S.acc_full, tp, abort, p.status)) break;
+      __syncwarp();
+      tc_fence_after();
+      uint32_t v[HC];
+#pragma unroll
+      for (int c = 0; c < HC; c += 32) tmem_ld32(taddr + c, v + c);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_empty0);
+      if (NV) {
+#pragma unroll
+        for (int j = 0; j < HC; ++j)
+          v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(S.rx[tp][half * HC + j], rw)));
+      }
+      store_columns<HC>(p, v, m0, n, n - (odd ? 1 : 0), odd, pairs);
+    }
+  }
+
+  if (warp == 0 && lane == 0 && *abort) {
+    // a wait gave up: the copies in flight count on barriers that may never
+    // complete, so give them a millisecond to land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
+  tc_fence_before();
+  cluster_sync();                                  // both CTAs done with the paired TMEM
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// Tokens of a tile: a round of tiles takes about nk stages of 4 (45 + PN / 2)
+// cycles and 1000 for the accumulator's read and the ramp, so the cheapest of
+// 128, 192 and 256 depends on how full it leaves the last round.
+static int pair_tokens(const Args& a, int pairs) {
+  int best = 256;
+  int64_t best_cost = INT64_MAX;
+  for (int pn : {256, 192, 128}) {
+    const int64_t tiles = (int64_t)((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + pn - 1) / pn);
+    const int64_t cost = (tiles + pairs - 1) / pairs * ((int64_t)(a.na + (a.K + 255) / 256) * 4 * (45 + pn / 2) + 1000);
+    if (cost < best_cost) { best_cost = cost; best = pn; }
+  }
+  return best;
+}
+
+template <int FMT, int PN>
+static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
+                       int RP, const Args& a, cudaStream_t s, int num_sms) {
+  using Sh = PairShape<FMT, PN>;
+  CUtensorMap tw, tx, tsw, tsx, twa, txa;
+  const uint64_t kb = (uint64_t)a.K / 2;
+  if (!make_tmap_2d_u8(&tw, w->packed, kb, a.N, kb, BKB, BW, true) ||
+      !make_tmap_2d_u8(&tx, x->packed, kb, a.M, kb, BKB, Sh::PNH, true) ||
+      !make_scale_tmap(&tsw, w->scales, FMT, a.N, a.K, Sh::NT, 1) ||
+      !make_scale_tmap(&tsx, x->scales, FMT, a.M, a.K, Sh::NT, Sh::RB))
+    return QLORA_ERR_CUDA;
+  twa = tw;
+  txa = tx;
+  if (RP && (!make_tmap_2d_bf16(&twa, wad, RP, a.N, RP, 64, BW) ||
+             !make_tmap_2d_bf16(&txa, tokad, RP, a.M, RP, 64, Sh::PNH)))
+    return QLORA_ERR_CUDA;
+  constexpr size_t bytes = sizeof(PairSmem<FMT, PN>) + 1024;
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+  static std::atomic<unsigned long long> attr_devs{0};
+  set_smem_attr_once(k_mx_gemm_pair<FMT, PN>, (int)bytes, attr_devs);
+  const int tiles = ((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + PN - 1) / PN);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * std::max(1, std::min(tiles, num_sms / 2)), 1, 1);
+  cfg.blockDim = dim3(P_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_mx_gemm_pair<FMT, PN>, tw, tx, tsw, tsx, twa, txa, a) == cudaSuccess
+             ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+template <int FMT>
+static int launch_pair_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
+                           int RP, const Args& a, cudaStream_t s, int num_sms) {
+  switch (pair_tokens(a, std::max(1, num_sms / 2))) {
+    case 128: return launch_pair<FMT, 128>(x, w, tokad, wad, RP, a, s, num_sms);
+    case 192: return launch_pair<FMT, 192>(x, w, tokad, wad, RP, a, s, num_sms);
+    default: return launch_pair<FMT, 256>(x, w, tokad, wad, RP, a, s, num_sms);
+  }
+}
+
+int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
+                     int RP, const Args& a, cudaStream_t s, int num_sms) {
+  return x->format == QLORA_NVFP4 ? launch_pair_fmt<QLORA_NVFP4>(x, w, tokad, wad, RP, a, s, num_sms)
+                                  : launch_pair_fmt<QLORA_MXFP4>(x, w, tokad, wad, RP, a, s, num_sms);
+}
+
+}  // namespace mx
+}  // namespace qnf4
