@@ -14,7 +14,6 @@ the same two layers.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from dataclasses import dataclass
 
@@ -81,16 +80,20 @@ class MXTensor:
     format: int = _lib.QLORA_NVFP4
 
     def c_struct(self) -> _lib.MXTensor:
-        _need_cuda(self.packed, self.scales, self.row_scale)
-        if (self.packed.numel() != self.rows * self.cols // 2
-                or self.scales.numel() < mx_scale_bytes(self.format, self.rows, self.cols)
-                or self.format == _lib.QLORA_NVFP4 and (self.row_scale is None
-                                                        or self.row_scale.numel() != self.rows)):
-            raise ValueError("buffers do not fit a %d x %d matrix of format %d"
-                             % (self.rows, self.cols, self.format))
-        return _lib.MXTensor(packed=_ptr(self.packed), rows=self.rows, cols=self.cols,
-                             format=self.format, reserved=0, scales=_ptr(self.scales),
-                             row_scale=_ptr(self.row_scale))
+        rows, cols, nv = self.rows, self.cols, self.format == _lib.QLORA_NVFP4
+        p, sc, rs = self.packed, self.scales, self.row_scale
+        dev = p.get_device()
+        if not (p.is_contiguous() and sc.is_contiguous() and dev >= 0 and sc.get_device() == dev
+                and p.dtype is torch.uint8 and sc.dtype is torch.uint8
+                and p.numel() == rows * cols // 2
+                and sc.numel() >= (rows + 127) // 128 * (-(-cols // (64 if nv else 128))) * 512):
+            raise ValueError("packed and scales must be contiguous uint8 CUDA tensors of a "
+                             f"{rows} x {cols} matrix")
+        if nv and (rs is None or rs.numel() != rows or rs.dtype is not torch.float32
+                   or not rs.is_contiguous() or rs.get_device() != dev):
+            raise ValueError(f"row_scale must be a contiguous fp32 CUDA tensor of {rows} values")
+        return _lib.MXTensor(p.data_ptr(), rows, cols, self.format, 0, sc.data_ptr(),
+                             rs.data_ptr() if nv else None)
 
     def block_scales(self) -> torch.Tensor:
         """The scale bytes as a row-major [rows, cols / block] tensor (a copy)."""
@@ -244,49 +247,60 @@ def qlora_linear_bwd_dropout(w: NF4Tensor, X, dY, A, B, alpha: float, p: float, 
                "qlora_linear_bwd_dropout")
 
 
-def _need_rows(*ts):
-    """2-D CUDA tensors whose rows are contiguous (any row stride)."""
-    for t in ts:
-        if t is not None and (not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)
-                              or (t.shape[0] > 1 and t.stride(0) < t.shape[1])):
-            raise ValueError("tensors must be 2-D CUDA tensors with contiguous rows")
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _ld(t) -> int:
-    return 0 if t is None else max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]
+class _On:
+    """Device and stream of a call: entered, it gives the raw stream.  With a
+    stream that is not the current one, buffers allocated inside belong to it,
+    so that the allocator orders their reuse after the call's work."""
+
+    def __init__(self, dev: int, stream):
+        self.dev, self.stream, self.ctx = dev, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is not None:
+            if self.stream.device.index != self.dev:
+                raise ValueError("the stream is on another device than the tensors")
+            self.ctx = torch.cuda.stream(self.stream)
+        elif self.dev != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(self.dev)
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return _raw_stream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
-def _place(stream, *ts):
-    """Context in which a call's buffers are allocated and its work enqueued:
-    the tensors' device (all on one), and `stream` when it is given, so that
-    the allocator orders the buffers' reuse after that stream's work."""
-    ts = [t for t in ts if t is not None]
-    if any(t.device != ts[0].device for t in ts):
-        raise ValueError("tensors are on different devices")
-    if stream is not None:
-        return torch.cuda.stream(stream)
-    if ts[0].is_cuda and ts[0].device.index != torch.cuda.current_device():
-        return torch.cuda.device(ts[0].device)
-    return contextlib.nullcontext()
+def _dense(dev: int, dtype, shape: tuple, t, what: str) -> int | None:
+    """Address of a contiguous tensor of this device, type and shape, or of None."""
+    if t is None:
+        return None
+    if (t.get_device() != dev or dev < 0 or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor {shape} on CUDA device {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _need_shape(*pairs):
-    for t, shape in pairs:
-        if t is not None and tuple(t.shape) != tuple(shape):
-            raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
-
-
-def _need_dtype(dtype, *ts):
-    for t in ts:
-        if t is not None and t.dtype != dtype:
-            raise ValueError(f"expected {dtype}, got {t.dtype}")
+def _rows_of(t, what: str) -> int:
+    """Row stride in elements of a 2-D CUDA tensor whose rows are contiguous."""
+    if t.get_device() < 0 or t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D CUDA tensor")
+    n, k = t.shape
+    if (k > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < k):
+        raise ValueError(f"{what}: expected contiguous rows")
+    return t.stride(0) if n > 1 else k
 
 
 def _float_type(t) -> int:
-    dt = {torch.float32: _lib.QLORA_F32, torch.bfloat16: _lib.QLORA_BF16}.get(t.dtype)
-    if dt is None:
-        raise ValueError("expected fp32 or bf16")
-    return dt
+    if t.dtype is torch.bfloat16:
+        return _lib.QLORA_BF16
+    if t.dtype is torch.float32:
+        return _lib.QLORA_F32
+    raise ValueError("expected fp32 or bf16")
 
 
 def mx_scale_bytes(format: int, rows: int, cols: int) -> int:
@@ -295,103 +309,106 @@ def mx_scale_bytes(format: int, rows: int, cols: int) -> int:
 
 def qlora_mx_quantize(X: torch.Tensor, out: MXTensor, stream=None):
     """Quantise X (fp32/bf16, rows contiguous, any row stride) into `out`."""
-    _need_rows(X)
-    _need_shape((X, (out.rows, out.cols)))
+    ld, dev = _rows_of(X, "X"), X.get_device()
+    if X.shape != (out.rows, out.cols) or out.packed.get_device() != dev:
+        raise ValueError("out does not fit X")
     cw = out.c_struct()
-    with _place(stream, X, out.packed, out.scales, out.row_scale):
-        _lib.check(_lib.load().qlora_mx_quantize(_ptr(X), _float_type(X), out.rows, out.cols, _ld(X),
-                                                 int(out.format), cw.packed, cw.scales, cw.row_scale,
-                                                 _stream(stream)),
+    with _On(dev, stream) as s:
+        _lib.check(_lib.load().qlora_mx_quantize(X.data_ptr(), _float_type(X), out.rows, out.cols, ld,
+                                                 out.format, cw.packed, cw.scales, cw.row_scale, s),
                    "qlora_mx_quantize")
 
 
 def qlora_mx_dequantize(t: MXTensor, out: torch.Tensor, stream=None):
-    _need_cuda(out)
-    _need_shape((out, (t.rows, t.cols)))
-    _need_dtype(torch.bfloat16, out)
-    cw = t.c_struct()
-    with _place(stream, out, t.packed, t.scales, t.row_scale):
-        _lib.check(_lib.load().qlora_mx_dequantize(C.byref(cw), _ptr(out), _stream(stream)),
-                   "qlora_mx_dequantize")
+    cw, dev = t.c_struct(), t.packed.get_device()
+    o = _dense(dev, torch.bfloat16, (t.rows, t.cols), out, "out")
+    with _On(dev, stream) as s:
+        _lib.check(_lib.load().qlora_mx_dequantize(C.byref(cw), o, s), "qlora_mx_dequantize")
 
 
 def qlora_mx_matmul(x: MXTensor, w: MXTensor, Y: torch.Tensor, stream=None):
     """Y[M, N] bf16 = deq(x) deq(w)^T, both of one format."""
-    _need_cuda(Y)
-    _need_shape((Y, (x.rows, w.rows)))
-    _need_dtype(torch.bfloat16, Y)
-    cx, cw = x.c_struct(), w.c_struct()
-    with _place(stream, Y, x.packed, x.scales, x.row_scale, w.packed, w.scales, w.row_scale):
-        _lib.check(_lib.load().qlora_mx_matmul(C.byref(cx), C.byref(cw), _ptr(Y), _stream(stream)),
-                   "qlora_mx_matmul")
+    cx, cw, dev = x.c_struct(), w.c_struct(), x.packed.get_device()
+    if w.packed.get_device() != dev:
+        raise ValueError("x and w are on different devices")
+    y = _dense(dev, torch.bfloat16, (x.rows, w.rows), Y, "Y")
+    with _On(dev, stream) as s:
+        _lib.check(_lib.load().qlora_mx_matmul(C.byref(cx), C.byref(cw), y, s), "qlora_mx_matmul")
 
 
-def _mx_dropout(p: float, seed: int):
-    return None if p == 0 else C.byref(_lib.Dropout(p=float(p), reserved=0, seed=int(seed)))
+def _mx_layer(w: MXTensor, X, A, B, p, seed):
+    """Checked arguments that the layer's forward and backward share."""
+    cw, dev, bf = w.c_struct(), w.packed.get_device(), torch.bfloat16
+    M, r = X.shape[0], 0 if A is None else A.shape[0]
+    x = _dense(dev, bf, (M, w.cols), X, "X")
+    a = _dense(dev, bf, (r, w.cols), A, "A")
+    b = _dense(dev, bf, (w.rows, r), B, "B")
+    dr = None if p == 0 else C.byref(_lib.Dropout(float(p), 0, int(seed)))
+    return cw, dev, M, r, x, a, b, dr
 
 
 def qlora_mx_linear_fwd(w: MXTensor, X, A, B, alpha: float, Y, T_save=None, p: float = 0.0,
                         seed: int = 0, ws=None, stream=None):
     """The QLoRA layer on a microscaled base (A = B = None: no adapter)."""
-    _need_cuda(X, A, B, Y, T_save)
-    _need_dtype(torch.bfloat16, X, A, B, Y, T_save)
-    M, r = X.shape[0], 0 if A is None else A.shape[0]
-    _need_shape((X, (M, w.cols)), (A, (r, w.cols)), (B, (w.rows, r)), (Y, (M, w.rows)),
-                (T_save, (M, r)))
-    with _place(stream, X, A, B, Y, T_save, w.packed, w.scales, w.row_scale):
+    cw, dev, M, r, x, a, b, dr = _mx_layer(w, X, A, B, p, seed)
+    y = _dense(dev, torch.bfloat16, (M, w.rows), Y, "Y")
+    t = _dense(dev, torch.bfloat16, (M, r), T_save, "T_save")
+    with _On(dev, stream) as s:
         if ws is None:
             ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_FWD, M, w.rows, w.cols, r), X.device)
-        cw = w.c_struct()
-        _lib.check(_lib.load().qlora_mx_linear_fwd(C.byref(cw), _ptr(X), M, _ptr(A), _ptr(B), r,
-                                                   float(alpha), _mx_dropout(p, seed), _ptr(Y),
-                                                   _ptr(T_save), _ptr(ws), ws.numel(),
-                                                   _stream(stream)),
+        _lib.check(_lib.load().qlora_mx_linear_fwd(C.byref(cw), x, M, a, b, r, alpha, dr, y, t,
+                                                   ws.data_ptr(), ws.numel(), s),
                    "qlora_mx_linear_fwd")
 
 
 def qlora_mx_linear_bwd(w: MXTensor, X, dY, A, B, alpha: float, dX, dA, dB, T=None,
                         p: float = 0.0, seed: int = 0, ws=None, stream=None):
     """Its backward (A = B = dA = dB = None: dX alone)."""
-    _need_cuda(X, dY, A, B, dX, dA, dB, T)
-    _need_dtype(torch.bfloat16, X, dY, A, B, dX, dA, dB, T)
-    M, r = X.shape[0], 0 if A is None else A.shape[0]
-    _need_shape((X, (M, w.cols)), (dY, (M, w.rows)), (A, (r, w.cols)), (B, (w.rows, r)),
-                (dX, (M, w.cols)), (dA, (r, w.cols)), (dB, (w.rows, r)), (T, (M, r)))
-    with _place(stream, X, dY, A, B, dX, dA, dB, T, w.packed, w.scales, w.row_scale):
+    cw, dev, M, r, x, a, b, dr = _mx_layer(w, X, A, B, p, seed)
+    bf = torch.bfloat16
+    dy = _dense(dev, bf, (M, w.rows), dY, "dY")
+    dx = _dense(dev, bf, (M, w.cols), dX, "dX")
+    da = _dense(dev, bf, (r, w.cols), dA, "dA")
+    db = _dense(dev, bf, (w.rows, r), dB, "dB")
+    t = _dense(dev, bf, (M, r), T, "T")
+    with _On(dev, stream) as s:
         if ws is None:
             ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_BWD, M, w.rows, w.cols, r), X.device)
-        cw = w.c_struct()
-        _lib.check(_lib.load().qlora_mx_linear_bwd(C.byref(cw), _ptr(X), _ptr(dY), M, _ptr(A), _ptr(B),
-                                                   r, float(alpha), _mx_dropout(p, seed), _ptr(T),
-                                                   _ptr(dX), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(),
-                                                   _stream(stream)),
+        _lib.check(_lib.load().qlora_mx_linear_bwd(C.byref(cw), x, dy, M, a, b, r, alpha, dr, t, dx,
+                                                   da, db, ws.data_ptr(), ws.numel(), s),
                    "qlora_mx_linear_bwd")
+
+
+def _like(t, X, what: str):
+    """(address, row stride) of a tensor with X's device, type and shape."""
+    if t is None:
+        return None, 0
+    if t.get_device() != X.get_device() or t.dtype is not X.dtype or t.shape != X.shape:
+        raise ValueError(f"{what}: expected {X.dtype} {tuple(X.shape)} on {X.device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), _rows_of(t, what)
 
 
 def qlora_dropout_fwd(X, p: float, seed: int, Y, residual=None, first: int = 0, stream=None):
     """Y = dropout(X) + residual with the layer's mask; element (i, j) has
     number first + i * cols + j.  Y may be X or residual."""
-    _need_rows(X, Y, residual)
-    _need_shape((Y, X.shape), (residual, X.shape))
-    _need_dtype(X.dtype, Y, residual)
-    dr = _lib.Dropout(p=float(p), reserved=0, seed=int(seed))
-    with _place(stream, X, Y, residual):
-        _lib.check(_lib.load().qlora_dropout_fwd(_ptr(X), _ld(X), _ptr(residual), _ld(residual),
-                                                 _float_type(X), X.shape[0], X.shape[1], C.byref(dr),
-                                                 int(first), _ptr(Y), _ld(Y), _stream(stream)),
+    ldx = _rows_of(X, "X")
+    (y, ldy), (r, ldr) = _like(Y, X, "Y"), _like(residual, X, "residual")
+    dr = _lib.Dropout(float(p), 0, int(seed))
+    with _On(X.get_device(), stream) as s:
+        _lib.check(_lib.load().qlora_dropout_fwd(X.data_ptr(), ldx, r, ldr, _float_type(X), X.shape[0],
+                                                 X.shape[1], C.byref(dr), int(first), y, ldy, s),
                    "qlora_dropout_fwd")
 
 
 def qlora_dropout_bwd(dY, p: float, seed: int, dX, first: int = 0, stream=None):
     """dX = D c dY with the forward's mask, regenerated."""
-    _need_rows(dY, dX)
-    _need_shape((dX, dY.shape))
-    _need_dtype(dY.dtype, dX)
-    dr = _lib.Dropout(p=float(p), reserved=0, seed=int(seed))
-    with _place(stream, dY, dX):
-        _lib.check(_lib.load().qlora_dropout_bwd(_ptr(dY), _ld(dY), _float_type(dY), dY.shape[0],
-                                                 dY.shape[1], C.byref(dr), int(first), _ptr(dX),
-                                                 _ld(dX), _stream(stream)),
+    ldy = _rows_of(dY, "dY")
+    x, ldx = _like(dX, dY, "dX")
+    dr = _lib.Dropout(float(p), 0, int(seed))
+    with _On(dY.get_device(), stream) as s:
+        _lib.check(_lib.load().qlora_dropout_bwd(dY.data_ptr(), ldy, _float_type(dY), dY.shape[0],
+                                                 dY.shape[1], C.byref(dr), int(first), x, ldx, s),
                    "qlora_dropout_bwd")
 
 
@@ -510,23 +527,23 @@ def mx_empty(rows: int, cols: int, device, format: int = _lib.QLORA_NVFP4) -> MX
 
 def mx_quantize(X: torch.Tensor, format: int = _lib.QLORA_NVFP4, stream=None) -> MXTensor:
     """Quantise a weight or activations: format 0 MXFP4, 1 NVFP4."""
-    _need_rows(X)
-    with _place(stream, X):
+    _rows_of(X, "X")
+    with _On(X.get_device(), stream):
         t = mx_empty(X.shape[0], X.shape[1], X.device, format)
     qlora_mx_quantize(X, t, stream)
     return t
 
 
 def mx_dequantize(t: MXTensor, stream=None) -> torch.Tensor:
-    with _place(stream, t.packed):
-        out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16, device=t.packed.device)
+    with _On(t.packed.get_device(), stream):
+        out = torch.empty((t.rows, t.cols), dtype=torch.bfloat16, device=t.packed.device)
     qlora_mx_dequantize(t, out, stream)
     return out
 
 
 def mx_matmul(x: MXTensor, w: MXTensor, stream=None) -> torch.Tensor:
-    with _place(stream, x.packed):
-        Y = torch.empty(x.rows, w.rows, dtype=torch.bfloat16, device=x.packed.device)
+    with _On(x.packed.get_device(), stream):
+        Y = torch.empty((x.rows, w.rows), dtype=torch.bfloat16, device=x.packed.device)
     qlora_mx_matmul(x, w, Y, stream)
     return Y
 
@@ -535,10 +552,10 @@ def mx_linear_fwd(w: MXTensor, X, A=None, B=None, alpha: float = 0.0, p: float =
                   save_T: bool = True, stream=None):
     """(Y, T) of the layer on a microscaled base; T is None without an adapter."""
     T = None
-    with _place(stream, X):
-        Y = torch.empty(X.shape[0], w.rows, dtype=torch.bfloat16, device=X.device)
+    with _On(X.get_device(), stream):
+        Y = torch.empty((X.shape[0], w.rows), dtype=torch.bfloat16, device=X.device)
         if A is not None and save_T:
-            T = torch.empty(X.shape[0], A.shape[0], dtype=torch.bfloat16, device=X.device)
+            T = torch.empty((X.shape[0], A.shape[0]), dtype=torch.bfloat16, device=X.device)
     qlora_mx_linear_fwd(w, X, A, B, alpha, Y, T, p, seed, stream=stream)
     return Y, T
 
@@ -546,7 +563,7 @@ def mx_linear_fwd(w: MXTensor, X, A=None, B=None, alpha: float = 0.0, p: float =
 def mx_linear_bwd(w: MXTensor, X, dY, A=None, B=None, alpha: float = 0.0, p: float = 0.0,
                   seed: int = 0, T=None, stream=None):
     """(dX, dA, dB); dA and dB are None without an adapter."""
-    with _place(stream, X):
+    with _On(X.get_device(), stream):
         dX = torch.empty_like(X)
         dA = None if A is None else torch.empty_like(A)
         dB = None if B is None else torch.empty_like(B)
@@ -556,14 +573,16 @@ def mx_linear_bwd(w: MXTensor, X, dY, A=None, B=None, alpha: float = 0.0, p: flo
 
 def dropout_fwd(X, p: float, seed: int, residual=None, first: int = 0, stream=None) -> torch.Tensor:
     """dropout(X) (+ residual) with the mask of the layer's dropout."""
-    with _place(stream, X):
+    _rows_of(X, "X")
+    with _On(X.get_device(), stream):
         Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
     qlora_dropout_fwd(X, p, seed, Y, residual, first, stream)
     return Y
 
 
 def dropout_bwd(dY, p: float, seed: int, first: int = 0, stream=None) -> torch.Tensor:
-    with _place(stream, dY):
+    _rows_of(dY, "dY")
+    with _On(dY.get_device(), stream):
         dX = torch.empty(dY.shape, dtype=dY.dtype, device=dY.device)
     qlora_dropout_bwd(dY, p, seed, dX, first, stream)
     return dX

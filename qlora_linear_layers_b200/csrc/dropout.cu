@@ -25,37 +25,238 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 
-// One thread a Philox block: elements 8 blk .. 8 blk + 7 of the numbering that
-// starts at 0, of which [first, first + rows * cols) exist here.
+// The block's keep bits, as dropout_keep8 (common.cuh) draws them, with fewer
+// instructions.
+// What is left, 18 products of 64 x 64 bits a block, is bound by the integer
+// multiplier: 40 us for the 3.7 M blocks of a 8192 x 3584 tensor, of the 50 us
+// that bf16 dropout of it takes (fp32 8192 x 8192: 103 us, 5.2 TB/s).
+//  * the keys of the ten rounds are the same for every thread: they come as
+//    kernel arguments (constant operands);
+//  * key word 1 and counter words 1 to 3 start at 0, so round 1 has one product
+//    and in round 2 the other one has only constant factors;
+//  * a 24-bit uniform u >= thr is compared as a 32-bit word >= thr << 8 whose
+//    top 24 bits are u (thr < 2^24 as p < 1).
+struct DropoutKeys {
+  uint64_t k0[10];         // seed + r * W0
+  uint64_t h, l;           // the constant product of round 2: M0 * k0[0]
+  uint32_t thr8;           // thr << 8 (0 keeps everything)
+  float scale;
+};
+
+constexpr uint64_t kM0 = 0xD2E7470EE14C6C93ull, kM1 = 0xCA5A826395121157ull, kW1 = 0xBB67AE8584CAA73Bull;
+
+__device__ __forceinline__ void mul128(uint64_t a, uint64_t m, uint64_t& hi, uint64_t& lo) {
+  const unsigned __int128 p = (unsigned __int128)a * m;
+  hi = (uint64_t)(p >> 64);
+  lo = (uint64_t)p;
+}
+
+struct Draw {
+  uint64_t w[4];
+  __device__ __forceinline__ bool keep(int i, uint32_t thr8) const {
+    const uint32_t hi = (uint32_t)(w[i >> 1] >> 32), lo = (uint32_t)w[i >> 1];
+    return ((i & 1) ? __funnelshift_l(lo, hi, 24) : hi) >= thr8;
+  }
+};
+
+__device__ __forceinline__ Draw draw8(uint64_t blk, const DropoutKeys& k) {
+  uint64_t h0, l0, h1, l1, c0, c1, c2, c3;
+  mul128(blk, kM0, h0, l0);                        // round 1: (blk, 0, 0, 0)
+  c2 = h0;                                         // c0 = k0[0], c1 = 0, c3 = l0
+  c3 = l0;
+  mul128(c2, kM1, h1, l1);                         // round 2
+  c0 = h1 ^ k.k0[1];
+  c1 = l1;
+  c2 = k.h ^ c3 ^ kW1;
+  c3 = k.l;
+#pragma unroll
+  for (int r = 2; r < 10; ++r) {
+    mul128(c0, kM0, h0, l0);
+    mul128(c2, kM1, h1, l1);
+    c0 = h1 ^ c1 ^ k.k0[r];
+    c1 = l1;
+    c2 = h0 ^ c3 ^ (kW1 * (uint64_t)r);
+    c3 = l0;
+  }
+  return Draw{{c0, c1, c2, c3}};
+}
+
+static DropoutKeys make_keys(const Dropout& d) {
+  DropoutKeys k{};
+  for (int r = 0; r < 10; ++r) k.k0[r] = d.seed + (uint64_t)r * 0x9E3779B97F4A7C15ull;
+  const unsigned __int128 p = (unsigned __int128)kM0 * k.k0[0];
+  k.h = (uint64_t)(p >> 64);
+  k.l = (uint64_t)p;
+  k.thr8 = d.thr << 8;
+  k.scale = d.scale;
+  return k;
+}
+
+// The general kernel: any width, strides and first number.  One thread a
+// Philox block: elements 8 blk .. 8 blk + 7 of the numbering that starts at 0,
+// of which [first, first + rows * cols) exist here.
 template <typename T>
 __global__ void __launch_bounds__(256)
 k_dropout(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, int64_t n, int64_t cols,
-          int64_t first, Dropout d) {
+          int64_t first, const __grid_constant__ DropoutKeys d) {
   const int64_t b0 = first >> 3, b1 = (first + n + 7) >> 3;
   for (int64_t blk = b0 + (int64_t)blockIdx.x * blockDim.x + threadIdx.x; blk < b1;
        blk += (int64_t)gridDim.x * blockDim.x) {
-    const uint32_t keep = d.on ? dropout_keep8((uint64_t)blk, d.seed, d.thr) : 0xFFu;
+    const Draw draw = draw8((uint64_t)blk, d);
+    uint32_t keep = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) keep |= draw.keep(i, d.thr8) ? 1u << i : 0u;
+    // row and column of the block's first element here; they advance from there
+    const int64_t e0 = max((int64_t)0, blk * 8 - first), e1 = min(n, blk * 8 + 8 - first);
+    int64_t row = (e0 | cols) >> 32 ? e0 / cols : (int64_t)((uint32_t)e0 / (uint32_t)cols);
+    int64_t col = e0 - row * cols;
+    const int shift = (int)(first + e0 - blk * 8);
+    T x[8], r[8];
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t e = blk * 8 + i - first;
-      if (e < 0 || e >= n) continue;
-      const int64_t row = e / cols, col = e - row * cols;
-      float v = (keep >> i) & 1u ? __fmul_rn(to_f32(X[row * ldx + col]), d.scale) : 0.0f;
-      if (R) v = __fadd_rn(v, to_f32(R[row * ldr + col]));
-      Y[row * ldy + col] = from_f32<T>(v);
+      if (e0 + i < e1) {
+        x[i] = X[row * ldx + col];
+        if (R) r[i] = R[row * ldr + col];
+        if (++col == cols) { col = 0; ++row; }
+      }
+    }
+    row = (e0 | cols) >> 32 ? e0 / cols : (int64_t)((uint32_t)e0 / (uint32_t)cols);
+    col = e0 - row * cols;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (e0 + i < e1) {
+        float v = (keep >> (shift + i)) & 1u ? __fmul_rn(to_f32(x[i]), d.scale) : 0.0f;
+        if (R) v = __fadd_rn(v, to_f32(r[i]));
+        Y[row * ldy + col] = from_f32<T>(v);
+        if (++col == cols) { col = 0; ++row; }
+      }
     }
   }
 }
 
+// Eight elements of a row from 16-byte words, once a block lies in one row and
+// on its own 16-byte boundary: cols, strides and first multiples of 8.
+template <typename T> struct Oct;
+template <> struct Oct<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+  __device__ __forceinline__ void get(float* v) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) { v[2 * j] = bf16_lo(w[j]); v[2 * j + 1] = bf16_hi(w[j]); }
+  }
+  __device__ __forceinline__ void set(const float* v) {
+    a = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+};
+template <> struct Oct<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+  __device__ __forceinline__ void set(const float* v) {
+    a = make_float4(v[0], v[1], v[2], v[3]);
+    b = make_float4(v[4], v[5], v[6], v[7]);
+  }
+};
+
+// kUnroll blocks a thread and step, a grid-stride apart, so that one block's
+// loads and products cover the other's latencies.  DENSE: rows without gaps, one
+// index for all operands, and a last block of `tail` elements.
+
+
+#endif
+template <typename T, bool RES, bool DENSE>
+__global__ void __launch_bounds__(256)
+k_dropout8(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, int64_t blocks, int64_t row_blocks,
+           int tail, int64_t first_block, const __grid_constant__ DropoutKeys d) {
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < blocks; b += kUnroll * step) {
+    Oct<T> x[kUnroll], r[kUnroll];
+    int64_t row[kUnroll], col[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t k = b + i * step;
+      row[i] = 0;
+      col[i] = 8 * k;
+      if (!DENSE) {
+        row[i] = k / row_blocks;
+        col[i] = 8 * (k - row[i] * row_blocks);
+      }
+      if (i == 0 || k < blocks) {
+        x[i].load(X + row[i] * ldx + col[i]);
+        if (RES) r[i].load(R + row[i] * ldr + col[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const Draw draw = draw8((uint64_t)(first_block + b + i * step), d);
+      float v[8], w[8];
+      x[i].get(v);
+      if (RES) r[i].get(w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = draw.keep(j, d.thr8) ? __fmul_rn(v[j], d.scale) : 0.0f;
+        if (RES) v[j] = __fadd_rn(v[j], w[j]);
+      }
+      x[i].set(v);
+      if (i == 0 || b + i * step < blocks) x[i].store(Y + row[i] * ldy + col[i]);
+    }
+  }
+  if (DENSE && tail && blockIdx.x == gridDim.x - 1 && threadIdx.x < tail) {
+    const int j = threadIdx.x;
+    const int64_t e = 8 * blocks + j;
+    const Draw draw = draw8((uint64_t)(first_block + blocks), d);
+    bool keep = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) keep = i == j ? draw.keep(i, d.thr8) : keep;
+    float v = keep ? __fmul_rn(to_f32(X[e]), d.scale) : 0.0f;
+    if (RES) v = __fadd_rn(v, to_f32(R[e]));
+    Y[e] = from_f32<T>(v);
+  }
+}
+
+template <typename T>
+static void launch_dropout_t(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, int64_t rows,
+                             int64_t cols, int64_t first, const Dropout& drop, cudaStream_t s) {
+  const DropoutKeys d = make_keys(drop);
+  const int64_t n = rows * cols;
+  const int64_t blocks = (n + 14) / 8;
+  const bool dense = (ldx == cols && ldy == cols && (!R || ldr == cols)) || rows == 1;
+  if (first % 8 == 0 && (dense || (cols | ldx | ldy | (R ? ldr : 0)) % 8 == 0)) {
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n / 8 + 511) / 512, 148 * 8));
+    auto run = [&](auto kern) {
+      kern<<<grid, 256, 0, s>>>(X, ldx, R, ldr, Y, ldy, n / 8, cols / 8, (int)(n % 8), first / 8, d);
+    };
+    if (R) {
+      if (dense) run(k_dropout8<T, true, true>);
+      else run(k_dropout8<T, true, false>);
+    } else {
+      if (dense) run(k_dropout8<T, false, true>);
+      else run(k_dropout8<T, false, false>);
+    }
+    return;
+  }
+  const unsigned grid = (unsigned)std::min<int64_t>((blocks + 255) / 256, 148 * 8);
+  k_dropout<T><<<grid, 256, 0, s>>>(X, ldx, R, ldr, Y, ldy, n, cols, first, d);
+}
+
 void launch_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, void* Y, int64_t ldy, int dtype,
                     int64_t rows, int64_t cols, int64_t first, const Dropout& d, cudaStream_t s) {
-  const int64_t blocks = (rows * cols + 14) / 8;
-  const unsigned grid = (unsigned)std::min<int64_t>((blocks + 255) / 256, 148 * 8);
   if (dtype == QLORA_F32)
-    k_dropout<float><<<grid, 256, 0, s>>>((const float*)X, ldx, (const float*)R, ldr, (float*)Y, ldy, rows * cols,
-                                          cols, first, d);
+    launch_dropout_t((const float*)X, ldx, (const float*)R, ldr, (float*)Y, ldy, rows, cols, first, d, s);
   else
-    k_dropout<__nv_bfloat16><<<grid, 256, 0, s>>>((const __nv_bfloat16*)X, ldx, (const __nv_bfloat16*)R, ldr,
-                                                  (__nv_bfloat16*)Y, ldy, rows * cols, cols, first, d);
+    launch_dropout_t((const __nv_bfloat16*)X, ldx, (const __nv_bfloat16*)R, ldr, (__nv_bfloat16*)Y, ldy, rows, cols,
+                     first, d, s);
 }
 
 }  // namespace qnf4

@@ -6,19 +6,25 @@
 // elements and both block scales itself (tcgen05.mma kind::mxf4nvf4 /
 // kind::mxf4) and sums in fp32, so nothing is expanded: a stage of 256
 // contraction elements is 128 bytes a row.  The product is formed as
-// Y^T = w x^T: 128 weight rows are the MMA's M, BN tokens its N, so one kernel
-// serves one token (BN = 16) and thousands (BN = 256).
+// Y^T = w x^T: weight rows are the MMA's M, tokens its N.
 //
-//  * warp 0: TMA loads of both operands' codes (128-byte swizzle) and plain
-//    bulk copies of their scale tiles, one mbarrier a stage;
-//  * warp 1: one thread copies a stage's scale tiles into tensor memory
-//    (tcgen05.cp 32x128b, replicated to the four lane groups) and issues four
-//    K = 64 MMAs.  Scale columns alternate between two slots; a slot is
-//    written again only after the MMAs that read it have completed;
-//  * warps 2-5: epilogue, tensor memory -> registers -> bf16.
+// This file: dispatch, and the kernel for few tokens, which reads the weight
+// once and is bound by that read (or, below a few MB, by latency).  A tile is
+// 128 weight rows x BN tokens (16, 32 or 128); a cluster of S CTAs splits its
+// contraction, so that a few weight rows still occupy the GPU, and adds the
+// partial sums through distributed shared memory in rank order: one launch, no
+// workspace, the same bits every time.  Shared memory is sized for two CTAs an
+// SM: one streams while the other one ramps or reduces.
 //
-// The adapter s (X A^T) B^T runs first, as RP / 64 bf16 K steps (kind::f16)
-// into the same fp32 accumulator; its MMAs complete before the first
+//  * warp 0: TMA loads of both operands' codes (128-byte swizzle) and scale
+//    tiles, one mbarrier a stage;
+//  * warp 1: one thread copies a stage's scale tiles into the stage's own
+//    tensor-memory columns (tcgen05.cp 32x128b, replicated to the four lane
+//    groups) and issues four K = 64 MMAs;
+//  * warps 2-5: epilogue, tensor memory -> cluster reduction -> bf16.
+//
+// The adapter s (X A^T) B^T runs first, in rank 0, as RP / 64 bf16 K steps
+// (kind::f16) into the same accumulator; its MMAs complete before the first
 // block-scaled one is issued, since the two kinds need not run in order.
 // Every wait is bounded (QLORA_ERR_TIMEOUT).
 
@@ -41,25 +47,25 @@ constexpr int NUM_THREADS = 192;
 template <int FMT, int BN>
 struct Shape {
   static constexpr int NT = FMT == QLORA_NVFP4 ? 4 : 2;          // scale tiles of 256 elements
-  static constexpr int RB = (BN + 127) / 128;                     // 128-row scale blocks of the tokens
   static constexpr int W_BYTES = BW * BKB, X_BYTES = BN * BKB;
-  static constexpr int SW_BYTES = NT * 512, SX_BYTES = RB * NT * 512;
-  static constexpr int STAGE = W_BYTES + X_BYTES + SW_BYTES + SX_BYTES;
-  static constexpr int NS = BN > 128 ? 4 : BN > 64 ? 5 : 6;
+  static constexpr int S_BYTES = NT * 512;                        // scales of 128 rows
+  static constexpr int STAGE = W_BYTES + X_BYTES + 2 * S_BYTES;
+  static constexpr int NS = BN == 16 ? 4 : 3;                     // two CTAs an SM
+  static constexpr bool OWN_PART = BN <= 32;                      // the partial sums have memory of their own
   static constexpr int D_COLS = BN < 32 ? 32 : BN;
-  static constexpr int SF_COLS = 4 * NT * (1 + RB);               // one slot: the stage's scale columns
-  static constexpr int NEED = D_COLS + 2 * SF_COLS;
-  static constexpr int TMEM_COLS = NEED <= 64 ? 64 : NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
+  static constexpr int SF_COLS = 8 * NT;                          // a stage's scale columns
+  static constexpr int TMEM_COLS = 256;
+  static_assert(D_COLS + NS * SF_COLS <= TMEM_COLS, "tensor memory columns");
 };
 
 template <int FMT, int BN>
 struct Smem {
   using Sh = Shape<FMT, BN>;
-  uint8_t w[Sh::NS][Sh::W_BYTES];
+  uint8_t w[Sh::NS][Sh::W_BYTES];                  // w, then x: the partial sums when !OWN_PART
   uint8_t x[Sh::NS][Sh::X_BYTES];
-  uint8_t sw[Sh::NS][Sh::SW_BYTES];
-  uint8_t sx[Sh::NS][Sh::SX_BYTES];
-  float rx[BN];
+  uint8_t sw[Sh::NS][Sh::S_BYTES];
+  uint8_t sx[Sh::NS][Sh::S_BYTES];
+  float part[Sh::OWN_PART ? BN * 128 : 4];
   uint64_t full[Sh::NS], empty[Sh::NS], acc_full, kind;
   uint32_t tmem_base;
   int abort;
@@ -68,24 +74,57 @@ struct Smem {
 template <int FMT, int BN>
 constexpr size_t smem_bytes() { return sizeof(Smem<FMT, BN>) + 1024; }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+}
+
+// Add the ranks' partial sums of NC token columns (in rank order), scale, store.
+template <int NC, bool NV>
+__device__ __forceinline__ void add_ranks(const Args& p, const float* part, int rank_stride, int splits, int m, int n,
+                                          float rw, bool odd, bool pairs) {
+  float sum[NC], rx[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) rx[j] = NV && m + j < p.M ? __ldg(p.xr + m + j) : 0.0f;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) sum[j] = part[j * 128];
+  for (int z = 1; z < splits; ++z)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) sum[j] = __fadd_rn(sum[j], part[z * rank_stride + j * 128]);
+  uint32_t v[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) v[j] = __float_as_uint(NV ? __fmul_rn(sum[j], __fmul_rn(rx[j], rw)) : sum[j]);
+  store_columns<NC>(p, v, m, n, n - (odd ? 1 : 0), odd, pairs);
+}
+
 template <int FMT, int BN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(NUM_THREADS, 2)
 k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
           const __grid_constant__ CUtensorMap tm_x,       // [M, K / 2] bytes
           const __grid_constant__ CUtensorMap tm_sw,      // scale tiles of w
           const __grid_constant__ CUtensorMap tm_sx,      // scale tiles of x
           const __grid_constant__ CUtensorMap tm_wad,     // [N, RP] bf16
           const __grid_constant__ CUtensorMap tm_xad,     // [M, RP] bf16
-          const Args p) {
+          const Args p, const int log_splits) {
   using Sh = Shape<FMT, BN>;
-  constexpr int NS = Sh::NS, NT = Sh::NT, RB = Sh::RB;
+  constexpr int NS = Sh::NS, NT = Sh::NT;
   constexpr bool NV = FMT == QLORA_NVFP4;
+  constexpr int kLogBN = BN == 16 ? 4 : BN == 32 ? 5 : 7;
+  static_assert(BN * 512 <= NS * (Sh::W_BYTES + Sh::X_BYTES), "reduction buffer");
   extern __shared__ uint8_t smem_raw[];
   auto& S = *smem_align1024<Smem<FMT, BN>>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.x * BW, m0 = blockIdx.y * BN;
-  const int nk = (p.K + 255) / 256;
-  const int nsteps = p.na + nk;
+  const int splits = 1 << log_splits;
+  const int rank = (int)cluster_ctarank();
+  const int n0 = (int)(blockIdx.x >> log_splits) * BW, m0 = blockIdx.y * BN;
+  const int nk_all = (p.K + 255) / 256;
+  const int k0 = (int)(((int64_t)nk_all * rank) >> log_splits), k1 = (int)(((int64_t)nk_all * (rank + 1)) >> log_splits);
+  const int na = rank == 0 ? p.na : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -104,114 +143,148 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_sw);
+    tma_prefetch_desc(&tm_sx);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (splits > 1) cluster_arrive();                // a rank writes to another one once that one runs
   const uint32_t tmem = S.tmem_base;
   volatile int* abort = &S.abort;
 
   if (warp == 0) {
     if (elect_one()) {
-      int i = 0;
-      for (; i < nsteps; ++i) {
-        const int s = i % NS;
-        if (!mbar_wait(&S.empty[s], ((i / NS) & 1) ^ 1, abort, p.status)) break;
-        if (i < p.na) {
+      int s = 0, i = -na;
+      uint32_t ph = 0;
+      for (; i < k1 - k0; ++i) {
+        if (!mbar_wait(&S.empty[s], ph ^ 1, abort, p.status)) break;
+        if (i < 0) {
           mbar_arrive_expect_tx(&S.full[s], Sh::W_BYTES + Sh::X_BYTES);
-          tma_load_2d(S.w[s], &tm_wad, &S.full[s], i * 64, n0);
-          tma_load_2d(S.x[s], &tm_xad, &S.full[s], i * 64, m0);
+          tma_load_2d(S.w[s], &tm_wad, &S.full[s], (i + na) * 64, n0);
+          tma_load_2d(S.x[s], &tm_xad, &S.full[s], (i + na) * 64, m0);
         } else {
-          const int ks = i - p.na;
+          const int ks = k0 + i;
           mbar_arrive_expect_tx(&S.full[s], Sh::STAGE);
           tma_load_2d(S.w[s], &tm_w, &S.full[s], ks * BKB, n0);
-          tma_load_2d(S.x[s], &tm_x, &S.full[s], ks * BKB, m0);
           tma_load_3d(S.sw[s], &tm_sw, &S.full[s], 0, ks * NT, n0 / 128);
+          tma_load_2d(S.x[s], &tm_x, &S.full[s], ks * BKB, m0);
           tma_load_3d(S.sx[s], &tm_sx, &S.full[s], 0, ks * NT, m0 / 128);
         }
+        if (++s == NS) { s = 0; ph ^= 1; }
       }
-      if (i < nsteps || *abort)                                   // a wait gave up: let the copies in flight land
-        for (int j = max(0, i - NS); j < i; ++j) drain_wait(&S.full[j % NS], (j / NS) & 1, p.status);
+      if (*abort) {                                               // a wait gave up: let the copies in flight land
+        const int n = na + i;
+        for (int j = max(0, n - NS); j < n; ++j) drain_wait(&S.full[j % NS], (j / NS) & 1, p.status);
+      }
     }
   } else if (warp == 1) {
     if (elect_one()) {
       constexpr uint32_t kId16 = idesc_bf16_f32(BW, BN);
-      const uint32_t sf0 = tmem + Sh::D_COLS;
-      const uint32_t sub = (uint32_t)(m0 % 128) / 32;            // token tile's place in its scale block
+      const uint64_t a0 = sw128_kmajor_desc(smem_u32(S.w[0])), b0 = sw128_kmajor_desc(smem_u32(S.x[0]));
+      const uint64_t sw0 = scale_desc(smem_u32(S.sw[0])), sx0 = scale_desc(smem_u32(S.sx[0]));
+      int s = 0;
+      uint32_t ph = 0;
       bool ok = true;
-      for (int i = 0; i < nsteps && ok; ++i) {
-        const int s = i % NS;
-        ok = mbar_wait(&S.full[s], (i / NS) & 1, abort, p.status);
+      for (int i = -na; i < k1 - k0; ++i) {
+        ok = mbar_wait(&S.full[s], ph, abort, p.status);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t a = sw128_kmajor_desc(smem_u32(S.w[s])), b = sw128_kmajor_desc(smem_u32(S.x[s]));
-        if (i < p.na) {
+        const uint64_t a = a0 + (uint32_t)(s * (Sh::W_BYTES / 16)), b = b0 + (uint32_t)(s * (Sh::X_BYTES / 16));
+        if (i < 0) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ss(tmem, a + 2 * kk, b + 2 * kk, kId16, (i > 0 || kk > 0) ? 1u : 0u);
+          for (int q = 0; q < 4; ++q) mma_ss(tmem, a + 2 * q, b + 2 * q, kId16, (i > -na || q > 0) ? 1u : 0u);
           mma_commit(&S.empty[s]);
-          if (i == p.na - 1) {
+          if (i == -1) {
             mma_commit(&S.kind);
             ok = mbar_wait(&S.kind, 0, abort, p.status);
+            if (!ok) break;
             tc_fence_after();
           }
-          continue;
-        }
-        const int ks = i - p.na;
-        if (ks >= 2) {                                            // this slot's last readers are done
-          const int j = i - 2;
-          ok = mbar_wait(&S.empty[j % NS], (j / NS) & 1, abort, p.status);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const uint32_t sfw = sf0 + (ks & 1) * Sh::SF_COLS, sfx = sfw + 4 * NT;
-        const int nq = min(4, (p.K - ks * 256 + 63) / 64);        // K = 64 steps with elements
-        const int nt = NV ? nq : (nq + 1) / 2;
-        for (int t = 0; t < nt; ++t) {
-          scale_copy(sfw + 4 * t, scale_desc(smem_u32(S.sw[s] + t * 512)));
+        } else {
+          const uint64_t sw = sw0 + (uint32_t)(s * (Sh::S_BYTES / 16)), sx = sx0 + (uint32_t)(s * (Sh::S_BYTES / 16));
+          const uint32_t sfw = tmem + Sh::D_COLS + s * Sh::SF_COLS, sfx = sfw + 4 * NT;
+          const int nq = min(4, (p.K - (k0 + i) * 256 + 63) / 64);  // K = 64 steps with elements
 #pragma unroll
-          for (int r = 0; r < RB; ++r)                            // a tile's token blocks side by side
-            scale_copy(sfx + 4 * (RB * t + r), scale_desc(smem_u32(S.sx[s] + (r * NT + t) * 512)));
+          for (int q = 0; q < 4; ++q) {
+            const int c = NV ? q : q >> 1;                        // scale tile of this K step
+            if (q >= nq) break;
+            if (NV || !(q & 1)) {
+              scale_copy(sfw + 4 * c, sw + 32 * c);
+              scale_copy(sfx + 4 * c, sx + 32 * c);
+            }
+            mma_mx<FMT>(tmem, a + 2 * q, b + 2 * q, idesc_mx<FMT>(BW, BN, NV ? 0u : 2u * (q & 1)), sfw + 4 * c,
+                        sfx + 4 * c, (i > 0 || q > 0 || na > 0) ? 1u : 0u);
+          }
+          mma_commit(&S.empty[s]);
         }
-        for (int q = 0; q < nq; ++q) {
-          const int t = NV ? q : q >> 1;
-          const uint32_t sf = NV ? 0u : 2u * (q & 1);
-          mma_mx<FMT>(tmem, a + 2 * q, b + 2 * q, idesc_mx<FMT>(BW, BN, sf), sfw + 4 * t, sfx + 4 * RB * t + sub,
-                      (i > 0 || q > 0) ? 1u : 0u);
-        }
-        mma_commit(&S.empty[s]);
+        if (++s == NS) { s = 0; ph ^= 1; }
       }
       mma_commit(&S.acc_full);
       mbar_wait(&S.acc_full, 0, abort, p.status);                 // nothing in flight when the CTA ends
     }
   } else {
-    const int quad = warp & 3;
-    const int n = n0 + quad * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+    mbar_wait(&S.acc_full, 0, abort, p.status);
+  }
+  __syncwarp();
+  if (splits > 1) {
+    cluster_wait();
+    if (!Sh::OWN_PART) cluster_sync();             // every rank is done with its stages
+  }
+  const int quad = warp & 3;
+  const int n = n0 + quad * 32 + lane;
+  const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+  const bool odd = lane & 1;
+  const bool pairs = (p.N & 1) == 0;
+  const int live = min(BN, p.M - m0);              // token columns that exist
+  const int cs = BN >> log_splits;                 // columns each rank adds up and stores (even)
+  float* part = Sh::OWN_PART ? S.part : reinterpret_cast<float*>(S.w[0]);   // [splits][cs][128]
+  if (warp >= 2) {
+    tc_fence_after();
     float rw = 1.0f;
-    if (NV) {
-      if (n < p.N) rw = p.wr[n];
-      for (int i = threadIdx.x - 64; i < BN; i += 128) S.rx[i] = m0 + i < p.M ? p.xr[m0 + i] : 0.0f;
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-    }
-    if (mbar_wait(&S.acc_full, 0, abort, p.status)) {
-      __syncwarp();
-      tc_fence_after();
-      const bool odd = lane & 1;
-      const bool pairs = (p.N & 1) == 0;                          // two adjacent outputs share a 32-bit word
+    if (NV && n < p.N) rw = p.wr[n];
+    if (splits == 1) {
 #pragma unroll 1
-      for (int c = 0; c < BN; c += 16) {
-        if (m0 + c >= p.M) break;
+      for (int c = 0; c < live; c += 16) {
         uint32_t v[16];
         tmem_ld16(tmem + lanes + c, v);
         tmem_wait_ld();
         if (NV) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(S.rx[c + j], rw)));
+          for (int j = 0; j < 16; ++j) {
+            const float rx = c + j < live ? __ldg(p.xr + m0 + c + j) : 0.0f;
+            v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(rx, rw)));
+          }
         }
         store_columns<16>(p, v, m0 + c, n, n - (odd ? 1 : 0), odd, pairs);
       }
+    } else {
+#pragma unroll 1
+      for (int c = 0; c < live; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + lanes + c, v);
+        tmem_wait_ld();
+        const uint32_t mine = smem_u32(part + rank * cs * 128 + quad * 32 + lane);
+        const int lcs = kLogBN - log_splits;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < live)
+            st_cluster_f32(mapa_shared(mine + (uint32_t)(((c + j) & (cs - 1)) * 512), (c + j) >> lcs),
+                           __uint_as_float(v[j]));
+      }
+    }
+  }
+  if (splits > 1) {
+    cluster_sync();                                // the partial sums have arrived
+    if (warp >= 2) {
+      float rw = 1.0f;
+      if (NV && n < p.N) rw = p.wr[n];
+      const float* mine = part + quad * 32 + lane;
+      const int first = m0 + rank * cs, n_cols = min(cs, p.M - first);
+      if (cs >= 8)
+        for (int c = 0; c < n_cols; c += 8) add_ranks<8, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, odd, pairs);
+      else
+        for (int c = 0; c < n_cols; c += 2) add_ranks<2, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, odd, pairs);
     }
   }
   tc_fence_before();
@@ -222,39 +295,72 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   }
 }
 
+// Expected time of this kernel in units of 10 ns, with 2^*log_splits ranks a
+// tile (1 to 8, as many as keep at most about one CTA on each SM, when that is
+// faster).  Fitted on B200 to W 4096 x 4096, 1024 x 18944 and 3584 x 18944 for
+// 1 to 128 tokens: 3.3 us of launch, ramp and drain (4.6 with 128 tokens), 0.34
+// us a stage (0.5), and 1.8 us + 30 ns a token for the cluster's reduction (4.2).
+// E.g. W 4096 x 4096, one token: 8.9 us unsplit, 7.7, 6.9 and 7.4 with 2, 4 and
+// 8 ranks; W 18944 x 3584 (148 tiles), 16 tokens: 10.4 us unsplit, 11.4 split.
+static int64_t split_cost(const Args& a, int bn, int num_sms, int* log_splits) {
+  const int64_t tiles = (int64_t)((a.N + BW - 1) / BW) * ((a.M + bn - 1) / bn);
+  const int nk = (a.K + 255) / 256;
+  int64_t best = INT64_MAX;
+  for (int s = 0; s <= 3 && (nk >> s) > 0; ++s) {
+    if (s && (tiles << s) > num_sms + num_sms / 8) break;
+    const int64_t waves = s ? 1 : (tiles + num_sms - 1) / num_sms;
+    const int64_t stages = a.na + (nk + (1 << s) - 1) / (1 << s);
+    const int64_t cost = bn > 32 ? 460 + waves * stages * 50 + (s ? 420 : 0)
+                                 : 330 + waves * stages * 34 + (s ? 180 + 3 * bn : 0);
+    if (cost < best) { best = cost; *log_splits = s; }
+  }
+  return best;
+}
+
 template <int FMT, int BN>
 static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                  int RP, const Args& a, cudaStream_t s) {
+                  int RP, const Args& a, cudaStream_t s, int num_sms) {
+  using Sh = Shape<FMT, BN>;
   CUtensorMap tw, tx, tsw, tsx, twa, txa;
   const uint64_t kb = (uint64_t)a.K / 2;
-  if (!make_tmap_2d_u8(&tw, w->packed, kb, a.N, kb, BKB, BW, true)) return QLORA_ERR_CUDA;
-  if (!make_tmap_2d_u8(&tx, x->packed, kb, a.M, kb, BKB, BN, true)) return QLORA_ERR_CUDA;
-  using Sh = Shape<FMT, BN>;
-  if (!make_scale_tmap(&tsw, w->scales, FMT, a.N, a.K, Sh::NT, 1) ||
-      !make_scale_tmap(&tsx, x->scales, FMT, a.M, a.K, Sh::NT, Sh::RB))
+  if (!make_tmap_2d_u8(&tw, w->packed, kb, a.N, kb, BKB, BW, true) ||
+      !make_tmap_2d_u8(&tx, x->packed, kb, a.M, kb, BKB, BN, true) ||
+      !make_scale_tmap(&tsw, w->scales, FMT, a.N, a.K, Sh::NT, 1) ||
+      !make_scale_tmap(&tsx, x->scales, FMT, a.M, a.K, Sh::NT, 1))
     return QLORA_ERR_CUDA;
   twa = tw;
   txa = tx;
-  if (RP) {
-    if (!make_tmap_2d_bf16(&twa, wad, RP, a.N, RP, 64, BW)) return QLORA_ERR_CUDA;
-    if (!make_tmap_2d_bf16(&txa, tokad, RP, a.M, RP, 64, BN)) return QLORA_ERR_CUDA;
-  }
-  static std::atomic<unsigned long long> attr_devs{0};
+  if (RP && (!make_tmap_2d_bf16(&twa, wad, RP, a.N, RP, 64, BW) ||
+             !make_tmap_2d_bf16(&txa, tokad, RP, a.M, RP, 64, BN)))
+    return QLORA_ERR_CUDA;
   constexpr size_t bytes = smem_bytes<FMT, BN>();
-  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+  static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs an SM");
+  static std::atomic<unsigned long long> attr_devs{0};
   set_smem_attr_once(k_mx_gemm<FMT, BN>, (int)bytes, attr_devs);
-  const dim3 grid((a.N + BW - 1) / BW, (a.M + BN - 1) / BN);
-  k_mx_gemm<FMT, BN><<<grid, NUM_THREADS, bytes, s>>>(tw, tx, tsw, tsx, twa, txa, a);
-  return QLORA_OK;
+  int log_splits = 0;
+  split_cost(a, BN, num_sms, &log_splits);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.N + BW - 1) / BW) << log_splits, (unsigned)((a.M + BN - 1) / BN), 1);
+  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1u << log_splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_mx_gemm<FMT, BN>, tw, tx, tsw, tsx, twa, txa, a, log_splits) == cudaSuccess
+             ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 template <int FMT>
 static int launch_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                      int RP, const Args& a, cudaStream_t s) {
-  if (a.M <= 16) return launch<FMT, 16>(x, w, tokad, wad, RP, a, s);
-  if (a.M <= 32) return launch<FMT, 32>(x, w, tokad, wad, RP, a, s);
-  if (a.M <= 64) return launch<FMT, 64>(x, w, tokad, wad, RP, a, s);
-  return launch<FMT, 128>(x, w, tokad, wad, RP, a, s);
+                      int RP, const Args& a, cudaStream_t s, int num_sms) {
+  if (a.M <= 16) return launch<FMT, 16>(x, w, tokad, wad, RP, a, s, num_sms);
+  if (a.M <= 32) return launch<FMT, 32>(x, w, tokad, wad, RP, a, s, num_sms);
+  return launch<FMT, 128>(x, w, tokad, wad, RP, a, s, num_sms);
 }
 
 }  // namespace mx
@@ -267,9 +373,15 @@ int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const voi
   a.M = (int)x->rows; a.N = (int)w->rows; a.K = (int)x->cols;
   a.na = RP / 64;
   a.status = status;
-  if (a.M > 128) return mx::launch_gemm_pair(x, w, tokad, wad, RP, a, s, num_sms);
-  return x->format == QLORA_NVFP4 ? mx::launch_fmt<QLORA_NVFP4>(x, w, tokad, wad, RP, a, s)
-                                  : mx::launch_fmt<QLORA_MXFP4>(x, w, tokad, wad, RP, a, s);
+  // Up to 32 tokens the weight's read bounds the product.  From 33 the paired
+  // kernel is faster wherever it has tiles enough (W 4096 x 4096, 128 tokens:
+  // 9.2 us against 10.6), a split contraction where a long one meets few weight
+  // rows (W 1024 x 18944, 128 tokens: 12.7 us against 23.1).
+  int ls = 0;
+  if (a.M > 32 && mx::pair_cost(a, num_sms) <= mx::split_cost(a, 128, num_sms, &ls))
+    return mx::launch_gemm_pair(x, w, tokad, wad, RP, a, s, num_sms);
+  return x->format == QLORA_NVFP4 ? mx::launch_fmt<QLORA_NVFP4>(x, w, tokad, wad, RP, a, s, num_sms)
+                                  : mx::launch_fmt<QLORA_MXFP4>(x, w, tokad, wad, RP, a, s, num_sms);
 }
 
 }  // namespace qnf4

@@ -25,6 +25,8 @@ struct Args {
   int* status;
 };
 
+// mx_gemm_pair.cu
+int64_t pair_cost(const Args& a, int num_sms);
 int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
                      int RP, const Args& a, cudaStream_t s, int num_sms);
 

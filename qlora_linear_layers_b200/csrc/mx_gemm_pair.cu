@@ -259,15 +259,23 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 // Tokens of a tile: a round of tiles takes about nk stages of 4 (45 + PN / 2)
 // cycles and 1000 for the accumulator's read and the ramp, so the cheapest of
 // 128, 192 and 256 depends on how full it leaves the last round.
-static int pair_tokens(const Args& a, int pairs) {
+static int pair_tokens(const Args& a, int num_sms, int64_t* cycles) {
+  const int pairs = std::max(1, num_sms / 2);
   int best = 256;
-  int64_t best_cost = INT64_MAX;
+  *cycles = INT64_MAX;
   for (int pn : {256, 192, 128}) {
     const int64_t tiles = (int64_t)((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + pn - 1) / pn);
     const int64_t cost = (tiles + pairs - 1) / pairs * ((int64_t)(a.na + (a.K + 255) / 256) * 4 * (45 + pn / 2) + 1000);
-    if (cost < best_cost) { best_cost = cost; best = pn; }
+    if (cost < *cycles) { *cycles = cost; best = pn; }
   }
   return best;
+}
+
+// Expected time in units of 10 ns: those cycles and 5.2 us of launch and ramp.
+int64_t pair_cost(const Args& a, int num_sms) {
+  int64_t cycles;
+  pair_tokens(a, num_sms, &cycles);
+  return 520 + cycles * 10 / 196;
 }
 
 template <int FMT, int PN>
@@ -310,7 +318,8 @@ static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const
 template <int FMT>
 static int launch_pair_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
                            int RP, const Args& a, cudaStream_t s, int num_sms) {
-  switch (pair_tokens(a, std::max(1, num_sms / 2))) {
+  int64_t cycles;
+  switch (pair_tokens(a, num_sms, &cycles)) {
     case 128: return launch_pair<FMT, 128>(x, w, tokad, wad, RP, a, s, num_sms);
     case 192: return launch_pair<FMT, 192>(x, w, tokad, wad, RP, a, s, num_sms);
     default: return launch_pair<FMT, 256>(x, w, tokad, wad, RP, a, s, num_sms);
