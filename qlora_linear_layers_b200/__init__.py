@@ -83,10 +83,12 @@ class MXTensor:
         rows, cols, nv = self.rows, self.cols, self.format == _lib.QLORA_NVFP4
         p, sc, rs = self.packed, self.scales, self.row_scale
         dev = p.get_device()
+        # a width that the library refuses has no tiles
+        tiles = 0 if cols % 32 else (rows + 127) // 128 * -(-cols // (64 if nv else 128))
         if not (p.is_contiguous() and sc.is_contiguous() and dev >= 0 and sc.get_device() == dev
                 and p.dtype is torch.uint8 and sc.dtype is torch.uint8
                 and p.numel() == rows * cols // 2
-                and sc.numel() >= (rows + 127) // 128 * (-(-cols // (64 if nv else 128))) * 512):
+                and sc.numel() >= tiles * 512):
             raise ValueError("packed and scales must be contiguous uint8 CUDA tensors of a "
                              f"{rows} x {cols} matrix")
         if nv and (rs is None or rs.numel() != rows or rs.dtype is not torch.float32

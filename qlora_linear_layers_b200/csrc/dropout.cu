@@ -172,9 +172,7 @@ template <> struct Oct<float> {
 // kUnroll blocks a thread and step, a grid-stride apart, so that one block's
 // loads and products cover the other's latencies.  DENSE: rows without gaps, one
 // index for all operands, and a last block of `tail` elements.
-
-
-#endif
+constexpr int kUnroll = 2;
 template <typename T, bool RES, bool DENSE>
 __global__ void __launch_bounds__(256)
 k_dropout8(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, int64_t blocks, int64_t row_blocks,
