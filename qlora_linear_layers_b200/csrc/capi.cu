@@ -688,7 +688,7 @@ int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
   DeviceInfo* d = nullptr;
   st = current_device(&d);
   if (st) return st;
-  st = launch_mx_gemm(x, w, nullptr, nullptr, 0, Y, d->status, (cudaStream_t)stream, d->sms);
+  st = launch_mx_gemm(x, w, MxAdapter{}, false, Y, d->status, (cudaStream_t)stream, d->sms);
   if (st) return st;
   st = launch_status();
   if (!st) count_launches(1);
@@ -731,21 +731,32 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   const bool nv = w->format == QLORA_NVFP4;
   float* xr = nv ? reinterpret_cast<float*>(wsb + lay.xr) : nullptr;
-  launch_mx_quantize(X, QLORA_BF16, M, K, K, w->format, wsb + lay.xq, wsb + lay.xs, xr, d->status, s);
+  const float scale = r ? alpha / (float)r : 0.0f;
+  // few tokens: quantisation and T in one launch, the adapter in the product's
+  // epilogue, the weight's read begun before either is done
+  const bool few = M <= kMxFewTokens && K <= kMxPrepMaxK && !dr.on;
+  MxAdapter ad;
   int n = 2;
-  const void* Bp = B;
-  const int RP = r ? padded_rank(r) : 0;
-  if (r) {
-    void* sT = wsb + lay.sT;
-    n += launch_lora_down(X, A, (int)M, (int)K, r, RP, alpha / (float)r, sT, T_save,
+  if (few) {
+    launch_mx_prep(X, (int)M, (int)K, A, r, w->format, wsb + lay.xq, wsb + lay.xs, xr, scale, wsb + lay.sT, T_save,
+                   d->status, s);
+    ad.r = r; ad.sT = wsb + lay.sT; ad.B = B;
+  } else {
+    launch_mx_quantize(X, QLORA_BF16, M, K, K, w->format, wsb + lay.xq, wsb + lay.xs, xr, d->status, s);
+  }
+  if (r && !few) {
+    ad.RP = padded_rank(r);
+    ad.tok = wsb + lay.sT;
+    ad.wt = B;
+    n += launch_lora_down(X, A, (int)M, (int)K, r, ad.RP, scale, wsb + lay.sT, T_save,
                           reinterpret_cast<float*>(wsb + lay.part), s, dropout ? &dr : nullptr);
     if (nv) {
-      launch_mx_pad_rows(sT, M, RP, RP, RP, xr, sT, s);
+      launch_mx_pad_rows(wsb + lay.sT, M, ad.RP, ad.RP, ad.RP, xr, wsb + lay.sT, s);
       ++n;
     }
-    if (nv || r < RP) {
-      launch_mx_pad_rows(B, N, r, r, RP, nv ? w->row_scale : nullptr, wsb + lay.Bpad, s);
-      Bp = wsb + lay.Bpad;
+    if (nv || r < ad.RP) {
+      launch_mx_pad_rows(B, N, r, r, ad.RP, nv ? w->row_scale : nullptr, wsb + lay.Bpad, s);
+      ad.wt = wsb + lay.Bpad;
       ++n;
     }
   }
@@ -758,7 +769,7 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
   cudaEvent_t e0, e1;
   take_gemm_events(&e0, &e1);
   if (e0) cudaEventRecord(e0, s);
-  st = launch_mx_gemm(&x, w, r ? wsb + lay.sT : nullptr, r ? Bp : nullptr, RP, Y, d->status, s, d->sms);
+  st = launch_mx_gemm(&x, w, ad, few, Y, d->status, s, d->sms);
   if (e1) cudaEventRecord(e1, s);
   if (st) return st;
   st = launch_status();

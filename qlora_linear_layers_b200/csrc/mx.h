@@ -25,6 +25,14 @@ __host__ __device__ constexpr int64_t mx_scale_offset(int64_t r, int64_t c, int6
 void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
                         uint8_t* packed, uint8_t* scales, float* row_scale, int* status,
                         cudaStream_t s);
+// Few tokens (M <= kMxFewTokens): X [M, K] bf16 quantised (scales of rows past M
+// are left as they are) and, with r > 0 and T = X A^T, sT [M, r] = RNbf16(s T)
+// and T_save = RNbf16(T) (may be null).  K <= kMxPrepMaxK.
+constexpr int kMxFewTokens = 32;
+constexpr int kMxPrepMaxK = 3 * 256 * 32;
+void launch_mx_prep(const void* X, int M, int K, const void* A, int r, int format, uint8_t* packed, uint8_t* scales,
+                    float* row_scale, float s, void* sT, void* T_save, int* status, cudaStream_t st);
+
 void launch_mx_dequantize(const qlora_mx_tensor* t, void* out, cudaStream_t s);
 
 // Wt[cols, rows] = deq(W)^T, bf16 (the values of qlora_mx_dequantize).
@@ -35,10 +43,23 @@ void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s);
 void launch_mx_pad_rows(const void* in, int64_t rows, int r, int ldi, int RP, const float* row_scale,
                         void* out, cudaStream_t s);
 
-// Y[M, N] = deq(x) deq(w)^T + tokad[M, RP] wad[N, RP]^T (bf16 factors, RP a
-// multiple of 64 or 0).  With NVFP4 the adapter factors come divided by the
-// row scales of x and w.  Returns QLORA_OK or QLORA_ERR_CUDA.
-int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad,
-                   const void* wad, int RP, void* Y, int* status, cudaStream_t s, int num_sms);
+// The adapter term of a product: none (RP = r = 0), bf16 factors of RP columns
+// (a multiple of 64) as extra K steps, tok [M, RP] and wt [N, RP] (with NVFP4
+// divided by the row scales of x and w), or, for few tokens, sT [M, r] and B
+// [N, r] as they are, added by the epilogue.
+struct MxAdapter {
+  int RP = 0;
+  const void* tok = nullptr;
+  const void* wt = nullptr;
+  int r = 0;
+  const void* sT = nullptr;
+  const void* B = nullptr;
+};
+
+// Y[M, N] = deq(x) deq(w)^T + the adapter's term.  after_prep: launched as the
+// dependent of launch_mx_prep, which wrote x and sT.  Returns QLORA_OK or
+// QLORA_ERR_CUDA.
+int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
+                   int* status, cudaStream_t s, int num_sms);
 
 }  // namespace qnf4

@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "gemm.h"
 #include "mx.h"
+#include "mx_mma.cuh"
 #include "mx_gemm.cuh"
 
 namespace qnf4 {
@@ -52,6 +53,7 @@ struct Shape {
   static constexpr int STAGE = W_BYTES + X_BYTES + 2 * S_BYTES;
   static constexpr int NS = BN == 16 ? 4 : 3;                     // two CTAs an SM
   static constexpr bool OWN_PART = BN <= 32;                      // the partial sums have memory of their own
+  static constexpr int ADD_PITCH = BW + 4;
   static constexpr int D_COLS = BN < 32 ? 32 : BN;
   static constexpr int SF_COLS = 8 * NT;                          // a stage's scale columns
   static constexpr int TMEM_COLS = 256;
@@ -66,6 +68,7 @@ struct Smem {
   uint8_t sw[Sh::NS][Sh::S_BYTES];
   uint8_t sx[Sh::NS][Sh::S_BYTES];
   float part[Sh::OWN_PART ? BN * 128 : 4];
+  float add[Sh::OWN_PART ? BN * Sh::ADD_PITCH : 4];               // the adapter's term, [token][weight row]
   uint64_t full[Sh::NS], empty[Sh::NS], acc_full, kind;
   uint32_t tmem_base;
   int abort;
@@ -74,6 +77,11 @@ struct Smem {
 template <int FMT, int BN>
 constexpr size_t smem_bytes() { return sizeof(Smem<FMT, BN>) + 1024; }
 
+// Wait for the grid that this one was launched after (returns at once when the
+// launch had no such attribute).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -84,13 +92,55 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
 }
 
+// The adapter's term of a warp's 32 weight rows, out[token][row] (pitch floats a
+// token): B [32 rows, r] times sT [BN tokens, r], both bf16, on mma.m16n8k16.
+// A lane takes 16-byte words of both operands, eight consecutive k each; the same
+// k in both, so their order within the product does not matter.
+template <int BN, int PITCH>
+__device__ __forceinline__ void adapter_term(const __nv_bfloat16* B, int rows, const __nv_bfloat16* sT, int tokens,
+                                             int r, float* out, int lane) {
+  const int g = lane >> 2, t = lane & 3;
+  float acc[2][BN / 8][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < BN / 8; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.0f;
+  auto word = [&](const __nv_bfloat16* p, int row, int n, int k) {
+    return row < n && k < r ? *reinterpret_cast<const uint4*>(p + (int64_t)row * r + k) : make_uint4(0, 0, 0, 0);
+  };
+  for (int k = 8 * t; k < r || k - 8 * t < r; k += 32) {
+    uint4 a[2][2], x[BN / 8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) a[i][h] = word(B, 16 * i + 8 * h + g, rows, k);
+#pragma unroll
+    for (int j = 0; j < BN / 8; ++j) x[j] = word(sT, 8 * j + g, tokens, k);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < BN / 8; ++j) {
+        mma_16816(acc[i][j], a[i][0].x, a[i][1].x, a[i][0].y, a[i][1].y, x[j].x, x[j].y);
+        mma_16816(acc[i][j], a[i][0].z, a[i][1].z, a[i][0].w, a[i][1].w, x[j].z, x[j].w);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < BN / 8; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)                  // row g or g + 8, token 2 t or 2 t + 1
+        out[(8 * j + 2 * t + (e & 1)) * PITCH + 16 * i + g + 8 * (e >> 1)] = acc[i][j][e];
+  __syncwarp();
+}
+
 // Add the ranks' partial sums of NC token columns (in rank order), scale, store.
 template <int NC, bool NV>
 __device__ __forceinline__ void add_ranks(const Args& p, const float* part, int rank_stride, int splits, int m, int n,
-                                          float rw, bool odd, bool pairs) {
+                                          float rw, const float* add, int add_pitch, bool odd, bool pairs) {
   float sum[NC], rx[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) rx[j] = NV && m + j < p.M ? __ldg(p.xr + m + j) : 0.0f;
+  for (int j = 0; j < NC; ++j) rx[j] = NV && m + j < p.M ? p.xr[m + j] : 0.0f;
 #pragma unroll
   for (int j = 0; j < NC; ++j) sum[j] = part[j * 128];
   for (int z = 1; z < splits; ++z)
@@ -98,7 +148,11 @@ __device__ __forceinline__ void add_ranks(const Args& p, const float* part, int 
     for (int j = 0; j < NC; ++j) sum[j] = __fadd_rn(sum[j], part[z * rank_stride + j * 128]);
   uint32_t v[NC];
 #pragma unroll
-  for (int j = 0; j < NC; ++j) v[j] = __float_as_uint(NV ? __fmul_rn(sum[j], __fmul_rn(rx[j], rw)) : sum[j]);
+  for (int j = 0; j < NC; ++j) {
+    if (NV) sum[j] = __fmul_rn(sum[j], __fmul_rn(rx[j], rw));
+    if (add) sum[j] = __fadd_rn(sum[j], add[j * add_pitch]);
+    v[j] = __float_as_uint(sum[j]);
+  }
   store_columns<NC>(p, v, m, n, n - (odd ? 1 : 0), odd, pairs);
 }
 
@@ -153,10 +207,21 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   const uint32_t tmem = S.tmem_base;
   volatile int* abort = &S.abort;
 
+  const int quad = warp & 3;
+  const int n = n0 + quad * 32 + lane;             // an epilogue lane's weight row
+  const int cs = BN >> log_splits;                 // token columns each rank adds up and stores (even)
   if (warp == 0) {
     if (elect_one()) {
       int s = 0, i = -na;
       uint32_t ph = 0;
+      // the first stages' weight loads do not wait for the grid that writes x
+      const int ahead = na ? 0 : min(NS, k1 - k0);
+      for (int j = 0; j < ahead; ++j) {
+        mbar_arrive_expect_tx(&S.full[j], Sh::STAGE);
+        tma_load_2d(S.w[j], &tm_w, &S.full[j], (k0 + j) * BKB, n0);
+        tma_load_3d(S.sw[j], &tm_sw, &S.full[j], 0, (k0 + j) * NT, n0 / 128);
+      }
+      grid_dependency_wait();
       for (; i < k1 - k0; ++i) {
         if (!mbar_wait(&S.empty[s], ph ^ 1, abort, p.status)) break;
         if (i < 0) {
@@ -165,9 +230,11 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
           tma_load_2d(S.x[s], &tm_xad, &S.full[s], (i + na) * 64, m0);
         } else {
           const int ks = k0 + i;
-          mbar_arrive_expect_tx(&S.full[s], Sh::STAGE);
-          tma_load_2d(S.w[s], &tm_w, &S.full[s], ks * BKB, n0);
-          tma_load_3d(S.sw[s], &tm_sw, &S.full[s], 0, ks * NT, n0 / 128);
+          if (i >= ahead) {
+            mbar_arrive_expect_tx(&S.full[s], Sh::STAGE);
+            tma_load_2d(S.w[s], &tm_w, &S.full[s], ks * BKB, n0);
+            tma_load_3d(S.sw[s], &tm_sw, &S.full[s], 0, ks * NT, n0 / 128);
+          }
           tma_load_2d(S.x[s], &tm_x, &S.full[s], ks * BKB, m0);
           tma_load_3d(S.sx[s], &tm_sx, &S.full[s], 0, ks * NT, m0 / 128);
         }
@@ -224,6 +291,13 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
       mbar_wait(&S.acc_full, 0, abort, p.status);                 // nothing in flight when the CTA ends
     }
   } else {
+    grid_dependency_wait();
+    if constexpr (Sh::OWN_PART) {                  // the adapter, while the MMAs run
+      const int row = n0 + quad * 32;
+      if (p.r && row < p.N)
+        adapter_term<BN, Sh::ADD_PITCH>(p.B + (int64_t)row * p.r, min(32, p.N - row), p.sT + (int64_t)m0 * p.r,
+                                        p.M - m0, p.r, S.add + quad * 32, lane);
+    }
     mbar_wait(&S.acc_full, 0, abort, p.status);
   }
   __syncwarp();
@@ -231,13 +305,10 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
     cluster_wait();
     if (!Sh::OWN_PART) cluster_sync();             // every rank is done with its stages
   }
-  const int quad = warp & 3;
-  const int n = n0 + quad * 32 + lane;
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const bool odd = lane & 1;
   const bool pairs = (p.N & 1) == 0;
   const int live = min(BN, p.M - m0);              // token columns that exist
-  const int cs = BN >> log_splits;                 // columns each rank adds up and stores (even)
   float* part = Sh::OWN_PART ? S.part : reinterpret_cast<float*>(S.w[0]);   // [splits][cs][128]
   if (warp >= 2) {
     tc_fence_after();
@@ -252,9 +323,14 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
         if (NV) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float rx = c + j < live ? __ldg(p.xr + m0 + c + j) : 0.0f;
+            const float rx = c + j < live ? p.xr[m0 + c + j] : 0.0f;
             v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(rx, rw)));
           }
+        }
+        if (Sh::OWN_PART && p.r) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), S.add[(c + j) * Sh::ADD_PITCH + quad * 32 + lane]));
         }
         store_columns<16>(p, v, m0 + c, n, n - (odd ? 1 : 0), odd, pairs);
       }
@@ -281,10 +357,15 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
       if (NV && n < p.N) rw = p.wr[n];
       const float* mine = part + quad * 32 + lane;
       const int first = m0 + rank * cs, n_cols = min(cs, p.M - first);
+      const float* add = Sh::OWN_PART && p.r ? S.add + rank * cs * Sh::ADD_PITCH + quad * 32 + lane : nullptr;
       if (cs >= 8)
-        for (int c = 0; c < n_cols; c += 8) add_ranks<8, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, odd, pairs);
+        for (int c = 0; c < n_cols; c += 8)
+          add_ranks<8, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, add ? add + c * Sh::ADD_PITCH : nullptr,
+                           Sh::ADD_PITCH, odd, pairs);
       else
-        for (int c = 0; c < n_cols; c += 2) add_ranks<2, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, odd, pairs);
+        for (int c = 0; c < n_cols; c += 2)
+          add_ranks<2, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, add ? add + c * Sh::ADD_PITCH : nullptr,
+                           Sh::ADD_PITCH, odd, pairs);
     }
   }
   tc_fence_before();
@@ -318,8 +399,8 @@ static int64_t split_cost(const Args& a, int bn, int num_sms, int* log_splits) {
 }
 
 template <int FMT, int BN>
-static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                  int RP, const Args& a, cudaStream_t s, int num_sms) {
+static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep,
+                  const Args& a, cudaStream_t s, int num_sms) {
   using Sh = Shape<FMT, BN>;
   CUtensorMap tw, tx, tsw, tsx, twa, txa;
   const uint64_t kb = (uint64_t)a.K / 2;
@@ -330,8 +411,8 @@ static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void
     return QLORA_ERR_CUDA;
   twa = tw;
   txa = tx;
-  if (RP && (!make_tmap_2d_bf16(&twa, wad, RP, a.N, RP, 64, BW) ||
-             !make_tmap_2d_bf16(&txa, tokad, RP, a.M, RP, 64, BN)))
+  if (ad.RP && (!make_tmap_2d_bf16(&twa, ad.wt, ad.RP, a.N, ad.RP, 64, BW) ||
+                !make_tmap_2d_bf16(&txa, ad.tok, ad.RP, a.M, ad.RP, 64, BN)))
     return QLORA_ERR_CUDA;
   constexpr size_t bytes = smem_bytes<FMT, BN>();
   static_assert(2 * (bytes + 1024) <= 228 * 1024, "two CTAs an SM");
@@ -344,44 +425,49 @@ static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1u << log_splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = after_prep ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_mx_gemm<FMT, BN>, tw, tx, tsw, tsx, twa, txa, a, log_splits) == cudaSuccess
              ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 template <int FMT>
-static int launch_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                      int RP, const Args& a, cudaStream_t s, int num_sms) {
-  if (a.M <= 16) return launch<FMT, 16>(x, w, tokad, wad, RP, a, s, num_sms);
-  if (a.M <= 32) return launch<FMT, 32>(x, w, tokad, wad, RP, a, s, num_sms);
-  return launch<FMT, 128>(x, w, tokad, wad, RP, a, s, num_sms);
+static int launch_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep,
+                      const Args& a, cudaStream_t s, int num_sms) {
+  if (a.M <= 16) return launch<FMT, 16>(x, w, ad, after_prep, a, s, num_sms);
+  if (a.M <= 32) return launch<FMT, 32>(x, w, ad, after_prep, a, s, num_sms);
+  return launch<FMT, 128>(x, w, ad, after_prep, a, s, num_sms);
 }
 
 }  // namespace mx
 
-int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad,
-                   const void* wad, int RP, void* Y, int* status, cudaStream_t s, int num_sms) {
+int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
+                   int* status, cudaStream_t s, int num_sms) {
   mx::Args a{};
   a.xr = x->row_scale; a.wr = w->row_scale;
   a.out = static_cast<__nv_bfloat16*>(Y);
   a.M = (int)x->rows; a.N = (int)w->rows; a.K = (int)x->cols;
-  a.na = RP / 64;
+  a.na = ad.RP / 64;
+  a.r = ad.r;
+  a.sT = static_cast<const __nv_bfloat16*>(ad.sT);
+  a.B = static_cast<const __nv_bfloat16*>(ad.B);
   a.status = status;
   // Up to 32 tokens the weight's read bounds the product.  From 33 the paired
   // kernel is faster wherever it has tiles enough (W 4096 x 4096, 128 tokens:
   // 9.2 us against 10.6), a split contraction where a long one meets few weight
   // rows (W 1024 x 18944, 128 tokens: 12.7 us against 23.1).
   int ls = 0;
-  if (a.M > 32 && mx::pair_cost(a, num_sms) <= mx::split_cost(a, 128, num_sms, &ls))
-    return mx::launch_gemm_pair(x, w, tokad, wad, RP, a, s, num_sms);
-  return x->format == QLORA_NVFP4 ? mx::launch_fmt<QLORA_NVFP4>(x, w, tokad, wad, RP, a, s, num_sms)
-                                  : mx::launch_fmt<QLORA_MXFP4>(x, w, tokad, wad, RP, a, s, num_sms);
+  if (a.M > kMxFewTokens && mx::pair_cost(a, num_sms) <= mx::split_cost(a, 128, num_sms, &ls))
+    return mx::launch_gemm_pair(x, w, ad, a, s, num_sms);
+  return x->format == QLORA_NVFP4 ? mx::launch_fmt<QLORA_NVFP4>(x, w, ad, after_prep, a, s, num_sms)
+                                  : mx::launch_fmt<QLORA_MXFP4>(x, w, ad, after_prep, a, s, num_sms);
 }
 
 }  // namespace qnf4

@@ -22,13 +22,16 @@ struct Args {
   __nv_bfloat16* out;
   int M, N, K;
   int na;                   // adapter K steps
+  int r;                    // rank of the adapter added by the epilogue (few tokens), 0: none
+  const __nv_bfloat16* sT;  // [M, r]
+  const __nv_bfloat16* B;   // [N, r]
   int* status;
 };
 
 // mx_gemm_pair.cu
 int64_t pair_cost(const Args& a, int num_sms);
-int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                     int RP, const Args& a, cudaStream_t s, int num_sms);
+int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
+                     cudaStream_t s, int num_sms);
 
 // True in one lane of a converged warp.  The tensor-core and TMA instructions
 // take their operands from uniform registers; behind an elect.sync the compiler

@@ -279,8 +279,8 @@ int64_t pair_cost(const Args& a, int num_sms) {
 }
 
 template <int FMT, int PN>
-static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                       int RP, const Args& a, cudaStream_t s, int num_sms) {
+static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
+                       cudaStream_t s, int num_sms) {
   using Sh = PairShape<FMT, PN>;
   CUtensorMap tw, tx, tsw, tsx, twa, txa;
   const uint64_t kb = (uint64_t)a.K / 2;
@@ -291,8 +291,8 @@ static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const
     return QLORA_ERR_CUDA;
   twa = tw;
   txa = tx;
-  if (RP && (!make_tmap_2d_bf16(&twa, wad, RP, a.N, RP, 64, BW) ||
-             !make_tmap_2d_bf16(&txa, tokad, RP, a.M, RP, 64, Sh::PNH)))
+  if (ad.RP && (!make_tmap_2d_bf16(&twa, ad.wt, ad.RP, a.N, ad.RP, 64, BW) ||
+                !make_tmap_2d_bf16(&txa, ad.tok, ad.RP, a.M, ad.RP, 64, Sh::PNH)))
     return QLORA_ERR_CUDA;
   constexpr size_t bytes = sizeof(PairSmem<FMT, PN>) + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
@@ -316,20 +316,20 @@ static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const
 }
 
 template <int FMT>
-static int launch_pair_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                           int RP, const Args& a, cudaStream_t s, int num_sms) {
+static int launch_pair_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
+                           cudaStream_t s, int num_sms) {
   int64_t cycles;
   switch (pair_tokens(a, num_sms, &cycles)) {
-    case 128: return launch_pair<FMT, 128>(x, w, tokad, wad, RP, a, s, num_sms);
-    case 192: return launch_pair<FMT, 192>(x, w, tokad, wad, RP, a, s, num_sms);
-    default: return launch_pair<FMT, 256>(x, w, tokad, wad, RP, a, s, num_sms);
+    case 128: return launch_pair<FMT, 128>(x, w, ad, a, s, num_sms);
+    case 192: return launch_pair<FMT, 192>(x, w, ad, a, s, num_sms);
+    default: return launch_pair<FMT, 256>(x, w, ad, a, s, num_sms);
   }
 }
 
-int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const void* tokad, const void* wad,
-                     int RP, const Args& a, cudaStream_t s, int num_sms) {
-  return x->format == QLORA_NVFP4 ? launch_pair_fmt<QLORA_NVFP4>(x, w, tokad, wad, RP, a, s, num_sms)
-                                  : launch_pair_fmt<QLORA_MXFP4>(x, w, tokad, wad, RP, a, s, num_sms);
+int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
+                     cudaStream_t s, int num_sms) {
+  return x->format == QLORA_NVFP4 ? launch_pair_fmt<QLORA_NVFP4>(x, w, ad, a, s, num_sms)
+                                  : launch_pair_fmt<QLORA_MXFP4>(x, w, ad, a, s, num_sms);
 }
 
 }  // namespace mx

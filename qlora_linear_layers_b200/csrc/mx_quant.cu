@@ -23,6 +23,7 @@
 
 #include "common.cuh"
 #include "mx.h"
+#include "mx_mma.cuh"
 
 namespace qnf4 {
 
@@ -161,29 +162,69 @@ __device__ __forceinline__ uint2 mx_codes16(const Unit<T>& u, int h, float inv) 
   return make_uint2(e2m1x8(v), e2m1x8(v + 8));
 }
 
-// One CTA a row (rows past the last write the zero scales of the padding).  A
-// thread takes units of 32 elements u = tid + i * blockDim; with KEEP > 0 the
-// row stays in registers (KEEP units a thread) between NVFP4's row maximum
-// and the codes, with KEEP == 0 it is read twice.
+// One row by a CTA (or by padding, live = false: zero scales only).  A thread
+// takes units of 32 elements k = tid + i * nt; with KEEP > 0 (KEEP * nt units at
+// least) the row stays in registers between NVFP4's row maximum and the codes,
+// with KEEP == 0 it is read twice.  s_max: shared, one word a warp.
 template <typename T, int FMT, int KEEP>
-__global__ void __launch_bounds__(512)
-k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __restrict__ packed,
-              uint8_t* __restrict__ scales, float* __restrict__ row_scale, int* status) {
+__device__ __forceinline__ void quantise_row(const T* __restrict__ x, bool live, int64_t row, int K, int tid, int nt,
+                                             uint8_t* __restrict__ packed, uint8_t* __restrict__ scales,
+                                             float* __restrict__ row_scale, int* status, uint32_t* s_max) {
   constexpr bool NV = FMT == QLORA_NVFP4;
   constexpr int kGroup = NV ? 2 : 4;               // units whose scale bytes share a 32-bit word
-  constexpr int kHold = KEEP > 0 ? KEEP : 1;
-  __shared__ uint32_t s_max[16];
-  const int64_t row = blockIdx.x;
   const int units = K / 32;
   const int upad = (units + kGroup - 1) / kGroup * kGroup;
   const int64_t tiles = mx_scale_tiles(FMT, K);
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const int rounds = (upad + nt - 1) / nt;
-  const T* x = X + row * ld;
-  Unit<T> u[kHold];
-  const bool live = row < rows;
-
+  Unit<T> u[KEEP > 0 ? KEEP : 1];
   float rs = 1.0f;
+
+  auto emit = [&](int k, const Unit<T>& w) {
+    const bool in = live && k < units;
+    uint32_t sb = 0;                               // this unit's scale bytes, in their place of the word
+    uint4 codes;
+    bool bad = false;
+    if constexpr (NV) {
+      uint2 c[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t a = w.amax16(h);
+        const bool nf = a >= kInfBits;
+        const uint32_t code = to_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(a), rs), 6.0f));
+        c[h] = nv_codes16(w, h, rs, from_e4m3(code));
+        if (nf) c[h] = make_uint2(0, 0);
+        bad |= nf;
+        sb |= (nf ? 0x7Fu : code) << (8 * (2 * (k & 1) + h));
+      }
+      codes = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+    } else {
+      const uint32_t a = max(w.amax16(0), w.amax16(1));
+      const bool nf = a >= kInfBits;
+      const uint32_t code = (uint32_t)max((int)(a >> 23) - 2, 0);
+      const float inv = __uint_as_float((254u - code) << 23);
+      const uint2 c0 = mx_codes16(w, 0, inv), c1 = mx_codes16(w, 1, inv);
+      codes = nf ? make_uint4(0, 0, 0, 0) : make_uint4(c0.x, c0.y, c1.x, c1.y);
+      bad |= nf;
+      sb |= (nf ? 0xFFu : code) << (8 * (k & 3));
+    }
+    if (!in) sb = 0;
+    sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 1);
+    if (!NV) sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
+    if (in) {
+      *reinterpret_cast<uint4*>(packed + row * (K / 2) + 16 * (int64_t)k) = codes;
+      if (bad) set_status(status, QLORA_ERR_NONFINITE);
+    }
+    if (k < upad && (k & (kGroup - 1)) == 0)
+      *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(row, (NV ? 2 : 1) * (int64_t)k, tiles)) = sb;
+  };
+  auto fetch = [&](int k, Unit<T>& w) {
+    if (live && k < units) w.load(x + 32 * (int64_t)k);
+    else w.zero();
+  };
+
+  if constexpr (KEEP > 0) {
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i) fetch(tid + i * nt, u[i]);
+  }
   if constexpr (NV) {
     uint32_t m = 0;
     auto take = [&](const Unit<T>& v) {
@@ -195,16 +236,10 @@ k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __r
     };
     if constexpr (KEEP > 0) {
 #pragma unroll
-      for (int i = 0; i < KEEP; ++i) {
-        const int k = tid + i * nt;
-        if (live && k < units) u[i].load(x + 32 * (int64_t)k);
-        else u[i].zero();
-      }
-#pragma unroll
       for (int i = 0; i < KEEP; ++i) take(u[i]);
-    } else if (live) {
+    } else {
       for (int k = tid; k < units; k += nt) {
-        u[0].load(x + 32 * (int64_t)k);
+        fetch(k, u[0]);
         take(u[0]);
       }
     }
@@ -220,61 +255,26 @@ k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __r
     rs = __uint_as_float((254u - f) << 23);
     if (live && tid == 0) row_scale[row] = __uint_as_float(f << 23);
   }
-
-  for (int i = 0; i < rounds; ++i) {
-    const int k = tid + i * nt;
-    const bool in = live && k < units;
-    Unit<T>* v = &u[0];
-    if constexpr (!NV || KEEP == 0) {
-      if (in) u[0].load(x + 32 * (int64_t)k);
-      else u[0].zero();
-    }
-    uint32_t sb = 0;                               // this unit's scale bytes, in their place of the word
-    uint4 codes;
-    bool bad = false;
-    auto body = [&](const Unit<T>& w) {
-      if constexpr (NV) {
-        uint2 c[2];
+  if constexpr (KEEP > 0) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t a = w.amax16(h);
-          const bool nf = a >= kInfBits;
-          const uint32_t code = to_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(a), rs), 6.0f));
-          c[h] = nv_codes16(w, h, rs, from_e4m3(code));
-          if (nf) c[h] = make_uint2(0, 0);
-          bad |= nf;
-          sb |= (nf ? 0x7Fu : code) << (8 * (2 * (k & 1) + h));
-        }
-        codes = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
-      } else {
-        const uint32_t a = max(w.amax16(0), w.amax16(1));
-        const bool nf = a >= kInfBits;
-        const uint32_t code = (uint32_t)max((int)(a >> 23) - 2, 0);
-        const float inv = __uint_as_float((254u - code) << 23);
-        const uint2 c0 = mx_codes16(w, 0, inv), c1 = mx_codes16(w, 1, inv);
-        codes = nf ? make_uint4(0, 0, 0, 0) : make_uint4(c0.x, c0.y, c1.x, c1.y);
-        bad |= nf;
-        sb |= (nf ? 0xFFu : code) << (8 * (k & 3));
-      }
-    };
-    if constexpr (NV && KEEP > 0) {
-#pragma unroll
-      for (int j = 0; j < KEEP; ++j)
-        if (j == i) body(u[j]);
-      (void)v;
-    } else {
-      body(u[0]);
+    for (int i = 0; i < KEEP; ++i)
+      if (i * nt < upad) emit(tid + i * nt, u[i]);
+  } else {
+    for (int k0 = 0; k0 < upad; k0 += nt) {
+      fetch(tid + k0, u[0]);
+      emit(tid + k0, u[0]);
     }
-    if (!in) sb = 0;
-    sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 1);
-    if (!NV) sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
-    if (in) {
-      *reinterpret_cast<uint4*>(packed + row * (K / 2) + 16 * (int64_t)k) = codes;
-      if (bad) set_status(status, QLORA_ERR_NONFINITE);
-    }
-    if (k < upad && (k & (kGroup - 1)) == 0)
-      *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(row, (NV ? 2 : 1) * (int64_t)k, tiles)) = sb;
   }
+}
+
+template <typename T, int FMT, int KEEP>
+__global__ void __launch_bounds__(512)
+k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __restrict__ packed,
+              uint8_t* __restrict__ scales, float* __restrict__ row_scale, int* status) {
+  __shared__ uint32_t s_max[16];
+  const int64_t row = blockIdx.x;                  // rows past the last write the padding's zero scales
+  quantise_row<T, FMT, KEEP>(X + row * ld, row < rows, row, K, threadIdx.x, blockDim.x, packed, scales, row_scale,
+                             status, s_max);
 }
 
 template <typename T, int FMT>
@@ -287,11 +287,9 @@ static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int6
     const int nt = std::min(512, std::max(32, ((upad + per - 1) / per + 31) / 32 * 32));
     kern<<<(unsigned)prow, nt, 0, s>>>((const T*)X, ld, (int)rows, (int)cols, packed, scales, row_scale, status);
   };
-  constexpr bool big = sizeof(T) == 4;
   if (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);
   else if (upad <= 256) run(k_mx_quantize<T, FMT, 1>, 1);
   else if (upad <= 1024) run(k_mx_quantize<T, FMT, 2>, 2);
-  else if (!big && upad <= 2048) run(k_mx_quantize<T, FMT, big ? 2 : 4>, 4);
   else run(k_mx_quantize<T, FMT, 0>, 1);
 }
 
@@ -304,6 +302,98 @@ void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, in
   } else {
     if (format == QLORA_NVFP4) launch_mx_quantize_t<__nv_bfloat16, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
     else launch_mx_quantize_t<__nv_bfloat16, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+  }
+}
+
+// ===========================================================================
+// What the layer does with few tokens before its product, in one launch: the
+// tokens quantised, a CTA a row, and T = X A^T.  A cluster takes eight rows of A
+// and cuts the contraction in 64 slices, one a warp (mma.m16n8k16 on 16-byte
+// words straight from global memory: a lane's words of X and A hold the same
+// eight k, so their order within the product does not matter); the warps' sums
+// are added in order, in the CTA and then by rank 0.  The product may start
+// meanwhile: it reads the weight first and waits for this grid before anything
+// written here.
+// ===========================================================================
+template <int FMT, int MT>
+__global__ void __cluster_dims__(8, 1, 1) __launch_bounds__(256)
+k_mx_prep(const __nv_bfloat16* __restrict__ X, int M, int K, const __nv_bfloat16* __restrict__ A, int r,
+          uint8_t* __restrict__ packed, uint8_t* __restrict__ scales, float* __restrict__ row_scale, float s,
+          __nv_bfloat16* __restrict__ sT, __nv_bfloat16* __restrict__ T_save, int* status) {
+  __shared__ uint32_t s_max[16];
+  __shared__ float s_warp[8][MT * 8];              // [warp][token * 8 + row of A]
+  __shared__ float s_rank[8][MT * 8];              // rank 0: the ranks' sums
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if ((int)blockIdx.x >= r) {
+    const int row = (int)blockIdx.x - r;
+    if (row < M)
+      quantise_row<__nv_bfloat16, FMT, 3>(X + (int64_t)row * K, true, row, K, tid, 256, packed, scales, row_scale,
+                                          status, s_max);
+    return;                                        // whole clusters: r is a multiple of 8
+  }
+  const int rank = (int)cluster_ctarank();
+  const int j0 = (int)blockIdx.x & ~7;
+  const int g = lane >> 2, t = lane & 3;
+  const int steps = K / 32, slice = rank * 8 + warp;
+  const int k0 = steps * slice / 64, k1 = steps * (slice + 1) / 64;
+  const __nv_bfloat16* a = A + (int64_t)(j0 + g) * K + 8 * t;
+  const __nv_bfloat16* x = X + (int64_t)g * K + 8 * t;
+  float acc[MT / 16][4];
+#pragma unroll
+  for (int i = 0; i < MT / 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+#pragma unroll 4
+  for (int k = k0; k < k1; ++k) {
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(a + 32 * (int64_t)k));
+    uint4 v[MT / 8];
+#pragma unroll
+    for (int i = 0; i < MT / 8; ++i)
+      v[i] = 8 * i + g < M ? __ldg(reinterpret_cast<const uint4*>(x + (int64_t)(8 * i) * K + 32 * (int64_t)k))
+                           : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < MT / 16; ++i) {
+      mma_16816(acc[i], v[2 * i].x, v[2 * i + 1].x, v[2 * i].y, v[2 * i + 1].y, b.x, b.y);
+      mma_16816(acc[i], v[2 * i].z, v[2 * i + 1].z, v[2 * i].w, v[2 * i + 1].w, b.z, b.w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)                    // token g or g + 8, row 2 t or 2 t + 1 of A
+      s_warp[warp][(16 * i + g + 8 * (e >> 1)) * 8 + 2 * t + (e & 1)] = acc[i][e];
+  cluster_sync();                                  // s_warp is whole, rank 0 runs
+  for (int i = tid; i < MT * 8; i += 256) {
+    float sum = s_warp[0][i];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) sum = __fadd_rn(sum, s_warp[w][i]);
+    asm volatile("st.shared::cluster.f32 [%0], %1;"
+                 :: "r"(mapa_shared(smem_u32(&s_rank[rank][i]), 0)), "f"(sum) : "memory");
+  }
+  cluster_sync();
+  if (rank == 0)
+    for (int i = tid; i < M * 8; i += 256) {
+      float sum = s_rank[0][i];
+#pragma unroll
+      for (int z = 1; z < 8; ++z) sum = __fadd_rn(sum, s_rank[z][i]);
+      const int64_t at = (int64_t)(i >> 3) * r + j0 + (i & 7);
+      sT[at] = __float2bfloat16_rn(__fmul_rn(s, sum));
+      if (T_save) T_save[at] = __float2bfloat16_rn(sum);
+    }
+}
+
+void launch_mx_prep(const void* X, int M, int K, const void* A, int r, int format, uint8_t* packed, uint8_t* scales,
+                    float* row_scale, float s, void* sT, void* T_save, int* status, cudaStream_t st) {
+  const unsigned grid = (unsigned)(r + (M + 7) / 8 * 8);
+  auto run = [&](auto kern) {
+    kern<<<grid, 256, 0, st>>>((const __nv_bfloat16*)X, M, K, (const __nv_bfloat16*)A, r, packed, scales, row_scale, s,
+                               (__nv_bfloat16*)sT, (__nv_bfloat16*)T_save, status);
+  };
+  if (format == QLORA_NVFP4) {
+    if (M <= 16) run(k_mx_prep<QLORA_NVFP4, 16>);
+    else run(k_mx_prep<QLORA_NVFP4, 32>);
+  } else {
+    if (M <= 16) run(k_mx_prep<QLORA_MXFP4, 16>);
+    else run(k_mx_prep<QLORA_MXFP4, 32>);
   }
 }
 
@@ -421,22 +511,30 @@ void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s) {
 // quantiser's row scales are powers of two, for which this is exact; any
 // other row scale costs one more bf16 rounding of the factor.
 // ===========================================================================
-__global__ void k_mx_pad_rows(const __nv_bfloat16* in, int64_t rows, int r, int ldi, int RP,
-                              const float* __restrict__ row_scale, __nv_bfloat16* out) {
-  const int64_t total = rows * RP;
+__global__ void __launch_bounds__(256)
+k_mx_pad_rows(const __nv_bfloat16* in, int64_t rows, int r, int ldi, int RP, const float* __restrict__ row_scale,
+              __nv_bfloat16* out) {
+  const int per = RP / 8;                          // 16-byte words of an output row (8 or 16)
+  const int64_t total = rows * per;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / RP;
-    const int c = (int)(i % RP);
-    float v = c < r ? __bfloat162float(in[row * ldi + c]) : 0.0f;
-    if (row_scale) v = __fdiv_rn(v, row_scale[row]);
-    out[i] = __float2bfloat16_rn(v);
+    const int64_t row = per == 8 ? i >> 3 : i >> 4;
+    const int c = 8 * (int)(i & (per - 1));
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (c < r) v = *reinterpret_cast<const uint4*>(in + row * ldi + c);
+    if (row_scale) {
+      const float s = row_scale[row];
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = pack_bf16x2(__fdiv_rn(bf16_lo(w[j]), s), __fdiv_rn(bf16_hi(w[j]), s));
+    }
+    *reinterpret_cast<uint4*>(out + row * RP + c) = v;
   }
 }
 
 void launch_mx_pad_rows(const void* in, int64_t rows, int r, int ldi, int RP, const float* row_scale,
                         void* out, cudaStream_t s) {
-  const int grid = (int)std::min<int64_t>((rows * RP + 255) / 256, 148 * 8);
+  const int grid = (int)std::min<int64_t>((rows * (RP / 8) + 255) / 256, 148 * 8);
   k_mx_pad_rows<<<grid, 256, 0, s>>>((const __nv_bfloat16*)in, rows, r, ldi, RP, row_scale, (__nv_bfloat16*)out);
 }
 
