@@ -90,7 +90,9 @@ typedef enum {
   QLORA_OP_FWD_DROPOUT = 3,
   QLORA_OP_BWD_DROPOUT = 4,
   QLORA_OP_MX_FWD = 5,        /* qlora_mx_linear_fwd, either format, r may be 0 */
-  QLORA_OP_MX_BWD = 6         /* qlora_mx_linear_bwd, likewise                  */
+  QLORA_OP_MX_BWD = 6,        /* qlora_mx_linear_bwd, likewise                  */
+  QLORA_OP_MX_FWD_DROPOUT = 7,  /* the same called with dropout                 */
+  QLORA_OP_MX_BWD_DROPOUT = 8
 } qlora_op;
 
 /* LoRA dropout on the adapter's input ([QE] config walk-through:
@@ -214,7 +216,8 @@ int qlora_dq_mean_from_hist(const int64_t* hist, int64_t n_total, float* mean);
 /* Bytes of caller workspace needed by an operation (0 if none).
  *   QLORA_OP_DOUBLE_QUANT: M, K, r ignored; N = number of absmax values.
  *   QLORA_OP_FWD / QLORA_OP_BWD: layer with M tokens, weight N x K, rank r.
- *   QLORA_OP_MX_FWD / QLORA_OP_MX_BWD: the same, r = 0 for no adapter. */
+ *   QLORA_OP_MX_FWD / QLORA_OP_MX_BWD: the same, r = 0 for no adapter (with a
+ *   dropout argument that is not NULL: the _DROPOUT ids). */
 size_t qlora_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r);
 
 /* Human-readable name of a status code (static string). */
@@ -429,7 +432,8 @@ int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
  * accumulator: with NVFP4 its bf16 factors are divided by the row scales
  * (exact for powers of two).
  * Constraints: M >= 1, N % 8 == 0, K % 64 == 0, r in {0, 8, 16, 32, 64, 128},
- * ws of qlora_workspace_bytes(QLORA_OP_MX_FWD, M, N, K, r) bytes.
+ * ws of qlora_workspace_bytes(QLORA_OP_MX_FWD, M, N, K, r) bytes, with dropout
+ * of QLORA_OP_MX_FWD_DROPOUT.
  */
 int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, const void* A,
                         const void* B, int r, float alpha, const qlora_dropout* dropout, void* Y,
@@ -441,7 +445,8 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
  * with the bf16 values of qlora_mx_dequantize for deq(W); arguments as for
  * qlora_linear_bwd_dropout, `dropout` may be NULL, r = 0 (A, B, T, dA, dB and
  * dropout NULL) computes dX alone.  T is the forward's T_save, or NULL to
- * recompute it.  ws of qlora_workspace_bytes(QLORA_OP_MX_BWD, M, N, K, r) bytes.
+ * recompute it.  ws of qlora_workspace_bytes(QLORA_OP_MX_BWD, M, N, K, r) bytes,
+ * with dropout of QLORA_OP_MX_BWD_DROPOUT.
  */
 int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY, int64_t M,
                         const void* A, const void* B, int r, float alpha,

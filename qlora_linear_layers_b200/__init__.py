@@ -357,7 +357,8 @@ def qlora_mx_linear_fwd(w: MXTensor, X, A, B, alpha: float, Y, T_save=None, p: f
     t = _dense(dev, torch.bfloat16, (M, r), T_save, "T_save")
     with _On(dev, stream) as s:
         if ws is None:
-            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_FWD, M, w.rows, w.cols, r), X.device)
+            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_FWD if dr is None
+                                            else _lib.QLORA_OP_MX_FWD_DROPOUT, M, w.rows, w.cols, r), X.device)
         _lib.check(_lib.load().qlora_mx_linear_fwd(C.byref(cw), x, M, a, b, r, alpha, dr, y, t,
                                                    ws.data_ptr(), ws.numel(), s),
                    "qlora_mx_linear_fwd")
@@ -375,7 +376,8 @@ def qlora_mx_linear_bwd(w: MXTensor, X, dY, A, B, alpha: float, dX, dA, dB, T=No
     t = _dense(dev, bf, (M, r), T, "T")
     with _On(dev, stream) as s:
         if ws is None:
-            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_BWD, M, w.rows, w.cols, r), X.device)
+            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_BWD if dr is None
+                                            else _lib.QLORA_OP_MX_BWD_DROPOUT, M, w.rows, w.cols, r), X.device)
         _lib.check(_lib.load().qlora_mx_linear_bwd(C.byref(cw), x, dy, M, a, b, r, alpha, dr, t, dx,
                                                    da, db, ws.data_ptr(), ws.numel(), s),
                    "qlora_mx_linear_bwd")

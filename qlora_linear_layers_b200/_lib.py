@@ -41,6 +41,8 @@ QLORA_OP_BWD_DROPOUT = 4
 
 QLORA_OP_MX_FWD = 5
 QLORA_OP_MX_BWD = 6
+QLORA_OP_MX_FWD_DROPOUT = 7
+QLORA_OP_MX_BWD_DROPOUT = 8
 
 QLORA_MXFP4 = 0
 QLORA_NVFP4 = 1

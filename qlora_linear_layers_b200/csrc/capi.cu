@@ -112,12 +112,13 @@ BwdWs bwd_ws(int64_t M, int64_t N, int64_t K, int r) {
 }
 
 // Forward workspace of the layer on a microscaled base: the quantised tokens
-// (codes, scale tiles, row scales), then the adapter's factors as in FwdWs,
-// both padded (NVFP4 also divides them by the row scales); r = 0 has none.
+// (codes, scale tiles, row scales), then the adapter's factors as the product
+// reads them (sT [M, RP], Bpad [N, RP]) and, with dropout, X' [M, K]; r = 0 has
+// none of these.
 struct MxFwdWs {
-  size_t xq, xs, xr, sT, Bpad, part, total;
+  size_t xq, xs, xr, sT, Bpad, xd, total;
 };
-MxFwdWs mx_fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
+MxFwdWs mx_fwd_ws(int64_t M, int64_t N, int64_t K, int r, bool dropout) {
   MxFwdWs w{};
   size_t off = 0;
   w.xq = off; off += align256((size_t)M * K / 2);
@@ -127,7 +128,29 @@ MxFwdWs mx_fwd_ws(int64_t M, int64_t N, int64_t K, int r) {
     const int RP = padded_rank(r);
     w.sT = off;   off += align256((size_t)M * RP * 2);
     w.Bpad = off; off += align256((size_t)N * RP * 2);
-    w.part = off; off += align256(skinny_workspace_bytes((int)M, (int)K, RP));
+    if (dropout) { w.xd = off; off += align256((size_t)M * K * 2); }
+  }
+  w.total = off;
+  return w;
+}
+
+// Its backward: Wt = deq(W)^T [K, N], and with an adapter T [M, r] (recomputed
+// when not passed), sU [M, RP], At [K, RP], Bt [r, N] and, with dropout, X'
+// [M, K] (all bf16).
+struct MxBwdWs {
+  size_t Wt, T, sU, At, Bt, xd, total;
+};
+MxBwdWs mx_bwd_ws(int64_t M, int64_t N, int64_t K, int r, bool dropout) {
+  MxBwdWs w{};
+  size_t off = 0;
+  w.Wt = off; off += align256((size_t)K * N * 2);
+  if (r) {
+    const int RP = padded_rank(r);
+    w.T = off;  off += align256((size_t)M * r * 2);
+    w.sU = off; off += align256((size_t)M * RP * 2);
+    w.At = off; off += align256((size_t)K * RP * 2);
+    w.Bt = off; off += align256((size_t)r * N * 2);
+    if (dropout) { w.xd = off; off += align256((size_t)M * K * 2); }
   }
   w.total = off;
   return w;
@@ -329,11 +352,13 @@ size_t qlora_workspace_bytes(int op, int64_t M, int64_t N, int64_t K, int r) {
       if (M < 1 || N < 1 || K < 1 || !valid_rank(r)) return 0;
       return fwd_ws(M, N, K, r, true).total;
     case QLORA_OP_MX_FWD:
+    case QLORA_OP_MX_FWD_DROPOUT:
       if (M < 1 || N < 1 || K < 1 || (r && !valid_rank(r))) return 0;
-      return mx_fwd_ws(M, N, K, r).total;
+      return mx_fwd_ws(M, N, K, r, op == QLORA_OP_MX_FWD_DROPOUT).total;
     case QLORA_OP_MX_BWD:
+    case QLORA_OP_MX_BWD_DROPOUT:
       if (M < 1 || N < 1 || K < 1 || (r && !valid_rank(r))) return 0;
-      return r ? bwd_ws(M, N, K, r).total : align256((size_t)K * N * 2);
+      return mx_bwd_ws(M, N, K, r, op == QLORA_OP_MX_BWD_DROPOUT).total;
     default: return 0;
   }
 }
@@ -514,32 +539,41 @@ static int fwd_impl(const nf4_weight* w, const void* X, int64_t M, const void* A
   return st;
 }
 
-}  // extern "C"
-
-// The backward after its argument checks: w_t writes deq(W)^T [K, N] in bf16.
-// r = 0 (microscaled layer without an adapter) computes dX = dY W' alone.
-template <typename DequantT>
-static int bwd_run(DequantT&& w_t, int64_t N, int64_t K, const void* X, const void* dY, int64_t M,
-                   const void* A, const void* B, int r, float alpha, const Dropout* drop, const void* T,
-                   void* dX, void* dA, void* dB, void* ws, qlora_stream_t stream, DeviceInfo* d) {
-  const BwdWs lay = r ? bwd_ws(M, N, K, r) : BwdWs{};
+static int bwd_impl(const nf4_weight* w, const void* X, const void* dY, int64_t M, const void* A,
+                    const void* B, int r, float alpha, const Dropout* drop, const void* T, void* dX,
+                    void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
+  int st = check_weight(w);
+  if (st) return st;
+  if (!X || !dY || !A || !B || !dX || !dA || !dB) return QLORA_ERR_INVALID_ARG;
+  if (!valid_rank(r) || !(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f) return QLORA_ERR_INVALID_ARG;
+  const int64_t N = w->rows, K = w->cols;
+  if (M < 1 || N % 8 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return QLORA_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
+      !aligned16(dA) || !aligned16(dB) || (T && !aligned16(T)))
+    return QLORA_ERR_ALIGN;
+  const BwdWs lay = bwd_ws(M, N, K, r);
+  if (!ws || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
+  DeviceInfo* d = nullptr;
+  st = current_device(&d);
+  if (st) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  const int RP = r ? padded_rank(r) : 0;
-  const float scale = r ? alpha / (float)r : 0.0f;
+  const int RP = padded_rank(r);
+  const float scale = alpha / (float)r;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   void* Tw = wsb + lay.T;
   void* sU = wsb + lay.sU;
   void* Wt = wsb + lay.Wt;
   void* At = wsb + lay.At;
-  int n = r ? 7 : 2;   // dequant_t, transpose_pad, GEMM, 2 x (partials + reduce)
-  if (r && !T) {
+  int n = 7;   // dequant_t, transpose_pad, GEMM, 2 x (partials + reduce)
+  if (!T) {
     n += launch_lora_down(X, A, (int)M, (int)K, r, RP, scale, nullptr, Tw,
                           reinterpret_cast<float*>(wsb + lay.pT), s, drop);
     T = Tw;
   }
-  if (r) n += launch_lora_u(dY, B, (int)M, (int)N, r, RP, scale, sU, reinterpret_cast<float*>(wsb + lay.pU), s);
-  w_t(Wt, s);
-  if (r) launch_transpose_pad(A, r, (int)K, RP, At, s);
+  n += launch_lora_u(dY, B, (int)M, (int)N, r, RP, scale, sU, reinterpret_cast<float*>(wsb + lay.pU), s);
+  launch_dequant_t(w, Wt, s);
+  launch_transpose_pad(A, r, (int)K, RP, At, s);
   // dX[M, K] = dY Wt^T + sU At^T   (tokens = dY rows, outputs = K, contraction = N)
   GemmArgs a{};
   a.out = static_cast<__nv_bfloat16*>(dX);
@@ -554,48 +588,23 @@ static int bwd_run(DequantT&& w_t, int64_t N, int64_t K, const void* X, const vo
   cudaEvent_t e0, e1;
   take_gemm_events(&e0, &e1);
   if (e0) cudaEventRecord(e0, s);
-  int st = K > 128 ? launch_qlora_gemm_pair(a, dY, r ? sU : dY, r ? At : Wt, Wt, r ? RP : 64, s, d->sms)
-                   : launch_qlora_gemm(MODE_BF16, a, dY, r ? sU : dY, r ? At : Wt, Wt, r ? RP : 64, s, d->sms);
+  st = K > 128 ? launch_qlora_gemm_pair(a, dY, sU, At, Wt, RP, s, d->sms)
+               : launch_qlora_gemm(MODE_BF16, a, dY, sU, At, Wt, RP, s, d->sms);
   if (e1) cudaEventRecord(e1, s);
   if (st) return st;
-  if (r) {
-    if (dropping) {
-      launch_rank_add(sU, RP, A, r, (int)M, (int)K, dX, *drop, s);
-      ++n;
-    }
-    // dA[r, K] = (s U)^T X ;  dB[N, r] = s dY^T T
-    launch_atb(sU, RP, r, X, (int)K, (int)K, (int)M, 1.0f, dA, reinterpret_cast<float*>(wsb + lay.pA),
-               d->sms, s, drop);
-    launch_atb(dY, (int)N, (int)N, T, r, r, (int)M, scale, dB, reinterpret_cast<float*>(wsb + lay.pB),
-               d->sms, s);
+  if (dropping) {
+    launch_rank_add(sU, RP, A, r, (int)M, (int)K, dX, *drop, s);
+    ++n;
   }
+  // dA[r, K] = (s U)^T X ;  dB[N, r] = s dY^T T
+  launch_atb(sU, RP, r, X, (int)K, (int)K, (int)M, 1.0f, dA, reinterpret_cast<float*>(wsb + lay.pA),
+             d->sms, s, drop);
+  launch_atb(dY, (int)N, (int)N, T, r, r, (int)M, scale, dB, reinterpret_cast<float*>(wsb + lay.pB),
+             d->sms, s);
   st = launch_status();
   if (!st) count_launches(n);
   return st;
 }
-
-static int bwd_impl(const nf4_weight* w, const void* X, const void* dY, int64_t M, const void* A,
-                    const void* B, int r, float alpha, const Dropout* drop, const void* T, void* dX,
-                    void* dA, void* dB, void* ws, size_t ws_bytes, qlora_stream_t stream) {
-  int st = check_weight(w);
-  if (st) return st;
-  if (!X || !dY || !A || !B || !dX || !dA || !dB) return QLORA_ERR_INVALID_ARG;
-  if (!valid_rank(r) || !(alpha == alpha) || alpha > 3.0e38f || alpha < -3.0e38f) return QLORA_ERR_INVALID_ARG;
-  const int64_t N = w->rows, K = w->cols;
-  if (M < 1 || N % 8 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return QLORA_ERR_SHAPE;
-  if (!aligned16(X) || !aligned16(dY) || !aligned16(A) || !aligned16(B) || !aligned16(dX) ||
-      !aligned16(dA) || !aligned16(dB) || (T && !aligned16(T)))
-    return QLORA_ERR_ALIGN;
-  if (!ws || ws_bytes < bwd_ws(M, N, K, r).total) return QLORA_ERR_WORKSPACE;
-  if (!aligned16(ws)) return QLORA_ERR_ALIGN;
-  DeviceInfo* d = nullptr;
-  st = current_device(&d);
-  if (st) return st;
-  return bwd_run([&](void* Wt, cudaStream_t s) { launch_dequant_t(w, Wt, s); }, N, K, X, dY, M, A, B, r,
-                 alpha, drop, T, dX, dA, dB, ws, stream, d);
-}
-
-extern "C" {
 
 int qlora_linear_fwd(const nf4_weight* w, const void* X, int64_t M, const void* A, const void* B,
                      int r, float alpha, void* Y, void* T_save, void* ws, size_t ws_bytes,
@@ -721,7 +730,7 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
   if (!Y || (!r && T_save)) return QLORA_ERR_INVALID_ARG;
   if (!aligned16(Y) || !aligned16(T_save)) return QLORA_ERR_ALIGN;
   const int64_t N = w->rows, K = w->cols;
-  const MxFwdWs lay = mx_fwd_ws(M, N, K, r);
+  const MxFwdWs lay = mx_fwd_ws(M, N, K, r, dropout != nullptr);
   if (!ws || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
   DeviceInfo* d = nullptr;
@@ -748,12 +757,15 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
     ad.RP = padded_rank(r);
     ad.tok = wsb + lay.sT;
     ad.wt = B;
-    n += launch_lora_down(X, A, (int)M, (int)K, r, ad.RP, scale, wsb + lay.sT, T_save,
-                          reinterpret_cast<float*>(wsb + lay.part), s, dropout ? &dr : nullptr);
-    if (nv) {
-      launch_mx_pad_rows(wsb + lay.sT, M, ad.RP, ad.RP, ad.RP, xr, wsb + lay.sT, s);
+    const void* Xd = X;
+    if (dr.on) {
+      launch_dropout(X, K, nullptr, 0, wsb + lay.xd, K, QLORA_BF16, M, K, 0, dr, s);
+      Xd = wsb + lay.xd;
       ++n;
     }
+    st = launch_mx_down(Xd, A, (int)M, (int)K, r, ad.RP, scale, xr, wsb + lay.sT, T_save, d->status, s, d->sms);
+    if (st) return st;
+    ++n;
     if (nv || r < ad.RP) {
       launch_mx_pad_rows(B, N, r, r, ad.RP, nv ? w->row_scale : nullptr, wsb + lay.Bpad, s);
       ad.wt = wsb + lay.Bpad;
@@ -785,13 +797,66 @@ int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY,
   if (st) return st;
   if (!dY || !dX || (r ? !dA || !dB : dA || dB || T)) return QLORA_ERR_INVALID_ARG;
   if (!aligned16(dY) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB) || !aligned16(T)) return QLORA_ERR_ALIGN;
-  if (!ws || ws_bytes < qlora_workspace_bytes(QLORA_OP_MX_BWD, M, w->rows, w->cols, r)) return QLORA_ERR_WORKSPACE;
+  const int64_t N = w->rows, K = w->cols;
+  const MxBwdWs lay = mx_bwd_ws(M, N, K, r, dropout != nullptr);
+  if (!ws || ws_bytes < lay.total) return QLORA_ERR_WORKSPACE;
   if (!aligned16(ws)) return QLORA_ERR_ALIGN;
   DeviceInfo* d = nullptr;
   st = current_device(&d);
   if (st) return st;
-  return bwd_run([&](void* Wt, cudaStream_t s) { launch_mx_dequant_t(w, Wt, s); }, w->rows, w->cols, X, dY, M,
-                 A, B, r, alpha, dropout ? &dr : nullptr, T, dX, dA, dB, ws, stream, d);
+  cudaStream_t s = (cudaStream_t)stream;
+  const int RP = r ? padded_rank(r) : 64;
+  const float scale = r ? alpha / (float)r : 0.0f;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
+  void *Wt = wsb + lay.Wt, *sU = wsb + lay.sU, *At = wsb + lay.At;
+  const void* Xd = X;
+  int n = 2;                                       // dequant_t and the GEMM
+  if (r) {
+    launch_mx_transpose(A, B, r, (int)K, (int)N, RP, At, wsb + lay.Bt, s);
+    if (dr.on) {
+      launch_dropout(X, K, nullptr, 0, wsb + lay.xd, K, QLORA_BF16, M, K, 0, dr, s);
+      Xd = wsb + lay.xd;
+      ++n;
+    }
+    if (!T) {
+      st = launch_mx_down(Xd, A, (int)M, (int)K, r, RP, scale, nullptr, nullptr, wsb + lay.T, d->status, s, d->sms);
+      if (st) return st;
+      T = wsb + lay.T;
+      ++n;
+    }
+    st = launch_mx_down(dY, wsb + lay.Bt, (int)M, (int)N, r, RP, scale, nullptr, sU, nullptr, d->status, s, d->sms);
+    if (st) return st;
+    n += 3;                                        // transpose, sU, outer
+  }
+  launch_mx_dequant_t(w, Wt, s);
+  // dX[M, K] = dY Wt^T + sU At^T; with dropout the adapter's term needs the keep
+  // mask: the GEMM writes dY W' alone and a rank-r pass adds D * c * (s U A)
+  GemmArgs a{};
+  a.out = static_cast<__nv_bfloat16*>(dX);
+  a.wad = static_cast<const __nv_bfloat16*>(At);
+  a.RP = RP;
+  a.Mtok = (int)M; a.Nout = (int)K; a.Kc = (int)N;
+  a.na = r && !dr.on ? RP / 64 : 0;
+  a.status = d->status;
+  const void *tokad = r ? sU : dY, *wad = r ? At : Wt;    // unread (na = 0) without an adapter
+  cudaEvent_t e0, e1;
+  take_gemm_events(&e0, &e1);
+  if (e0) cudaEventRecord(e0, s);
+  st = K > 128 ? launch_qlora_gemm_pair(a, dY, tokad, wad, Wt, RP, s, d->sms)
+               : launch_qlora_gemm(MODE_BF16, a, dY, tokad, wad, Wt, RP, s, d->sms);
+  if (e1) cudaEventRecord(e1, s);
+  if (st) return st;
+  if (dr.on) {
+    launch_rank_add(sU, RP, A, r, (int)M, (int)K, dX, dr, s);
+    ++n;
+  }
+  if (r) {
+    st = launch_mx_outer(Xd, (int)K, sU, RP, dA, dY, (int)N, T, scale, dB, (int)M, r, d->status, s, d->sms);
+    if (st) return st;
+  }
+  st = launch_status();
+  if (!st) count_launches(n);
+  return st;
 }
 
 static int dropout_impl(const void* X, int64_t ldx, const void* R, int64_t ldr, int dtype, int64_t rows,

@@ -88,9 +88,6 @@ __device__ __forceinline__ void cluster_arrive() {
 __device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
-}
 
 // The adapter's term of a warp's 32 weight rows, out[token][row] (pitch floats a
 // token): B [32 rows, r] times sT [BN tokens, r], both bf16, on mma.m16n8k16.

@@ -131,6 +131,11 @@ __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tma
       : "memory");
 }
 
+// Store into another CTA of the cluster (address from mapa_shared).
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
+}
+
 // Bounded wait for a copy in flight after the kernel has given up (the abort
 // flag is set and no longer looked at).
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity, const int* st) {

@@ -116,7 +116,10 @@ def test_workspace_sizes(lib):
         assert base >= M * K // 2 + lib.qlora_mx_scale_bytes(1, M, K) + 4 * M
         assert ws(_lib.QLORA_OP_MX_FWD, M, N, K, 16) > base
         assert ws(_lib.QLORA_OP_MX_BWD, M, N, K, 0) >= 2 * N * K
-        assert ws(_lib.QLORA_OP_MX_BWD, M, N, K, 16) >= ws(_lib.QLORA_OP_BWD, M, N, K, 16)
+        assert ws(_lib.QLORA_OP_MX_BWD, M, N, K, 16) > ws(_lib.QLORA_OP_MX_BWD, M, N, K, 0)
+        for plain, drop in ((_lib.QLORA_OP_MX_FWD, _lib.QLORA_OP_MX_FWD_DROPOUT),
+                            (_lib.QLORA_OP_MX_BWD, _lib.QLORA_OP_MX_BWD_DROPOUT)):
+            assert ws(drop, M, N, K, 16) >= ws(plain, M, N, K, 16) + 2 * M * K       # X'
         assert ws(_lib.QLORA_OP_MX_FWD, M, N, K, 12) == 0 == ws(_lib.QLORA_OP_MX_BWD, M, N, K, -1)
 
 

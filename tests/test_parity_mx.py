@@ -318,7 +318,7 @@ def test_streams_and_workspace_contents(q):
         G2 = q.mx_linear_bwd(w, X, dY, A, B, 16.0, p=0.1, seed=3, T=T2, stream=st)
         st.synchronize()
         assert torch.equal(Y, Y2) and torch.equal(T, T2) and all(torch.equal(a, b) for a, b in zip(G, G2))
-        n = q.workspace_bytes(q._lib.QLORA_OP_MX_FWD, 150, 264, 448, 16)
+        n = q.workspace_bytes(q._lib.QLORA_OP_MX_FWD_DROPOUT, 150, 264, 448, 16)
         ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
         Y3, T3 = torch.empty_like(Y), torch.empty_like(T)
         q.qlora_mx_linear_fwd(w, X, A, B, 16.0, Y3, T3, 0.1, 3, ws=ws)
