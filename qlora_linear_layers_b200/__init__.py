@@ -309,33 +309,68 @@ def mx_scale_bytes(format: int, rows: int, cols: int) -> int:
     return int(_lib.load().qlora_mx_scale_bytes(int(format), rows, cols))
 
 
+def _mx_quantize(X, out, format, stream):
+    ld, dev, (rows, cols) = _rows_of(X, "X"), X.get_device(), X.shape
+    lib = _lib.load()
+    with _On(dev, stream) as s:
+        if out is None:
+            nv = format == _lib.QLORA_NVFP4
+            out = MXTensor(X.new_empty(rows * cols // 2, dtype=torch.uint8),
+                           X.new_empty(lib.qlora_mx_scale_bytes(format, rows, cols), dtype=torch.uint8),
+                           X.new_empty(rows, dtype=torch.float32) if nv else None, rows, cols, format)
+            p, sc, rs = out.packed.data_ptr(), out.scales.data_ptr(), _ptr(out.row_scale)
+        else:
+            if (out.rows, out.cols) != (rows, cols) or out.packed.get_device() != dev:
+                raise ValueError("out does not fit X")
+            cw = out.c_struct()
+            p, sc, rs = cw.packed, cw.scales, cw.row_scale
+        _lib.check(lib.qlora_mx_quantize(X.data_ptr(), _float_type(X), rows, cols, ld, out.format, p, sc,
+                                         rs, s),
+                   "qlora_mx_quantize")
+    return out
+
+
 def qlora_mx_quantize(X: torch.Tensor, out: MXTensor, stream=None):
     """Quantise X (fp32/bf16, rows contiguous, any row stride) into `out`."""
-    ld, dev = _rows_of(X, "X"), X.get_device()
-    if X.shape != (out.rows, out.cols) or out.packed.get_device() != dev:
-        raise ValueError("out does not fit X")
-    cw = out.c_struct()
+    if out is None:
+        raise ValueError("out is missing")
+    _mx_quantize(X, out, out.format, stream)
+
+
+def _mx_dequantize(t: MXTensor, out, stream):
+    cw, dev = t.c_struct(), t.packed.get_device()
     with _On(dev, stream) as s:
-        _lib.check(_lib.load().qlora_mx_quantize(X.data_ptr(), _float_type(X), out.rows, out.cols, ld,
-                                                 out.format, cw.packed, cw.scales, cw.row_scale, s),
-                   "qlora_mx_quantize")
+        if out is None:
+            out = t.packed.new_empty((t.rows, t.cols), dtype=torch.bfloat16)
+        else:
+            _dense(dev, torch.bfloat16, (t.rows, t.cols), out, "out")
+        _lib.check(_lib.load().qlora_mx_dequantize(C.byref(cw), out.data_ptr(), s), "qlora_mx_dequantize")
+    return out
 
 
 def qlora_mx_dequantize(t: MXTensor, out: torch.Tensor, stream=None):
-    cw, dev = t.c_struct(), t.packed.get_device()
-    o = _dense(dev, torch.bfloat16, (t.rows, t.cols), out, "out")
+    if out is None:
+        raise ValueError("out is missing")
+    _mx_dequantize(t, out, stream)
+
+
+def _mx_matmul(x: MXTensor, w: MXTensor, Y, stream):
+    cx, cw, dev = x.c_struct(), w.c_struct(), x.packed.get_device()
+    if w.packed.get_device() != dev:
+        raise ValueError("x and w are on different devices")
     with _On(dev, stream) as s:
-        _lib.check(_lib.load().qlora_mx_dequantize(C.byref(cw), o, s), "qlora_mx_dequantize")
+        if Y is None:
+            Y = x.packed.new_empty((x.rows, w.rows), dtype=torch.bfloat16)
+            y = Y.data_ptr()
+        else:
+            y = _dense(dev, torch.bfloat16, (x.rows, w.rows), Y, "Y")
+        _lib.check(_lib.load().qlora_mx_matmul(C.byref(cx), C.byref(cw), y, s), "qlora_mx_matmul")
+    return Y
 
 
 def qlora_mx_matmul(x: MXTensor, w: MXTensor, Y: torch.Tensor, stream=None):
     """Y[M, N] bf16 = deq(x) deq(w)^T, both of one format."""
-    cx, cw, dev = x.c_struct(), w.c_struct(), x.packed.get_device()
-    if w.packed.get_device() != dev:
-        raise ValueError("x and w are on different devices")
-    y = _dense(dev, torch.bfloat16, (x.rows, w.rows), Y, "Y")
-    with _On(dev, stream) as s:
-        _lib.check(_lib.load().qlora_mx_matmul(C.byref(cx), C.byref(cw), y, s), "qlora_mx_matmul")
+    _mx_matmul(x, w, Y, stream)
 
 
 def _mx_layer(w: MXTensor, X, A, B, p, seed):
@@ -346,41 +381,70 @@ def _mx_layer(w: MXTensor, X, A, B, p, seed):
     a = _dense(dev, bf, (r, w.cols), A, "A")
     b = _dense(dev, bf, (w.rows, r), B, "B")
     dr = None if p == 0 else C.byref(_lib.Dropout(float(p), 0, int(seed)))
-    return cw, dev, M, r, x, a, b, dr
+    return C.byref(cw), dev, M, r, x, a, b, dr
+
+
+def _mx_fwd(w, X, A, B, alpha, Y, T, save_T, p, seed, ws, stream):
+    cw, dev, M, r, x, a, b, dr = _mx_layer(w, X, A, B, p, seed)
+    with _On(dev, stream) as s:
+        if Y is None:
+            Y = X.new_empty((M, w.rows))
+            if save_T and r:
+                T = X.new_empty((M, r))
+        else:
+            _dense(dev, torch.bfloat16, (M, w.rows), Y, "Y")
+            _dense(dev, torch.bfloat16, (M, r), T, "T_save")
+        if ws is None:
+            op = _lib.QLORA_OP_MX_FWD if dr is None else _lib.QLORA_OP_MX_FWD_DROPOUT
+            ws = _mx_workspace(op, M, w, r, X)
+        _lib.check(_lib.load().qlora_mx_linear_fwd(cw, x, M, a, b, r, alpha, dr, Y.data_ptr(), _ptr(T),
+                                                   ws.data_ptr(), ws.numel(), s),
+                   "qlora_mx_linear_fwd")
+    return Y, T
+
+
+def _mx_workspace(op, M, w, r, X):
+    return X.new_empty(max(16, _lib.load().qlora_workspace_bytes(op, M, w.rows, w.cols, r)),
+                       dtype=torch.uint8)
 
 
 def qlora_mx_linear_fwd(w: MXTensor, X, A, B, alpha: float, Y, T_save=None, p: float = 0.0,
                         seed: int = 0, ws=None, stream=None):
     """The QLoRA layer on a microscaled base (A = B = None: no adapter)."""
+    if Y is None:
+        raise ValueError("Y is missing")
+    _mx_fwd(w, X, A, B, alpha, Y, T_save, False, p, seed, ws, stream)
+
+
+def _mx_bwd(w, X, dY, A, B, alpha, dX, dA, dB, T, p, seed, ws, stream):
     cw, dev, M, r, x, a, b, dr = _mx_layer(w, X, A, B, p, seed)
-    y = _dense(dev, torch.bfloat16, (M, w.rows), Y, "Y")
-    t = _dense(dev, torch.bfloat16, (M, r), T_save, "T_save")
+    bf = torch.bfloat16
+    dy = _dense(dev, bf, (M, w.rows), dY, "dY")
+    t = _dense(dev, bf, (M, r), T, "T")
     with _On(dev, stream) as s:
+        if dX is None:
+            dX = torch.empty_like(X)
+            if r:
+                dA, dB = torch.empty_like(A), torch.empty_like(B)
+        else:
+            _dense(dev, bf, (M, w.cols), dX, "dX")
+            _dense(dev, bf, (r, w.cols), dA, "dA")
+            _dense(dev, bf, (w.rows, r), dB, "dB")
         if ws is None:
-            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_FWD if dr is None
-                                            else _lib.QLORA_OP_MX_FWD_DROPOUT, M, w.rows, w.cols, r), X.device)
-        _lib.check(_lib.load().qlora_mx_linear_fwd(C.byref(cw), x, M, a, b, r, alpha, dr, y, t,
-                                                   ws.data_ptr(), ws.numel(), s),
-                   "qlora_mx_linear_fwd")
+            op = _lib.QLORA_OP_MX_BWD if dr is None else _lib.QLORA_OP_MX_BWD_DROPOUT
+            ws = _mx_workspace(op, M, w, r, X)
+        _lib.check(_lib.load().qlora_mx_linear_bwd(cw, x, dy, M, a, b, r, alpha, dr, t, dX.data_ptr(),
+                                                   _ptr(dA), _ptr(dB), ws.data_ptr(), ws.numel(), s),
+                   "qlora_mx_linear_bwd")
+    return dX, dA, dB
 
 
 def qlora_mx_linear_bwd(w: MXTensor, X, dY, A, B, alpha: float, dX, dA, dB, T=None,
                         p: float = 0.0, seed: int = 0, ws=None, stream=None):
     """Its backward (A = B = dA = dB = None: dX alone)."""
-    cw, dev, M, r, x, a, b, dr = _mx_layer(w, X, A, B, p, seed)
-    bf = torch.bfloat16
-    dy = _dense(dev, bf, (M, w.rows), dY, "dY")
-    dx = _dense(dev, bf, (M, w.cols), dX, "dX")
-    da = _dense(dev, bf, (r, w.cols), dA, "dA")
-    db = _dense(dev, bf, (w.rows, r), dB, "dB")
-    t = _dense(dev, bf, (M, r), T, "T")
-    with _On(dev, stream) as s:
-        if ws is None:
-            ws = _workspace(workspace_bytes(_lib.QLORA_OP_MX_BWD if dr is None
-                                            else _lib.QLORA_OP_MX_BWD_DROPOUT, M, w.rows, w.cols, r), X.device)
-        _lib.check(_lib.load().qlora_mx_linear_bwd(C.byref(cw), x, dy, M, a, b, r, alpha, dr, t, dx,
-                                                   da, db, ws.data_ptr(), ws.numel(), s),
-                   "qlora_mx_linear_bwd")
+    if dX is None:
+        raise ValueError("dX is missing")
+    _mx_bwd(w, X, dY, A, B, alpha, dX, dA, dB, T, p, seed, ws, stream)
 
 
 def _like(t, X, what: str):
@@ -393,27 +457,39 @@ def _like(t, X, what: str):
     return t.data_ptr(), _rows_of(t, what)
 
 
+def _dropout(X, p, seed, Y, residual, first, stream, where):
+    ldx, dev = _rows_of(X, "X"), X.get_device()
+    r, ldr = _like(residual, X, "residual")
+    with _On(dev, stream) as s:
+        if Y is None:
+            Y = X.new_empty(X.shape)
+            y, ldy = Y.data_ptr(), X.shape[1]
+        else:
+            y, ldy = _like(Y, X, "output")
+        dr, (n, k), lib = C.byref(_lib.Dropout(float(p), 0, int(seed))), X.shape, _lib.load()
+        if where == "qlora_dropout_fwd":
+            st = lib.qlora_dropout_fwd(X.data_ptr(), ldx, r, ldr, _float_type(X), n, k, dr, int(first),
+                                       y, ldy, s)
+        else:
+            st = lib.qlora_dropout_bwd(X.data_ptr(), ldx, _float_type(X), n, k, dr, int(first), y, ldy,
+                                       s)
+        _lib.check(st, where)
+    return Y
+
+
 def qlora_dropout_fwd(X, p: float, seed: int, Y, residual=None, first: int = 0, stream=None):
     """Y = dropout(X) + residual with the layer's mask; element (i, j) has
     number first + i * cols + j.  Y may be X or residual."""
-    ldx = _rows_of(X, "X")
-    (y, ldy), (r, ldr) = _like(Y, X, "Y"), _like(residual, X, "residual")
-    dr = _lib.Dropout(float(p), 0, int(seed))
-    with _On(X.get_device(), stream) as s:
-        _lib.check(_lib.load().qlora_dropout_fwd(X.data_ptr(), ldx, r, ldr, _float_type(X), X.shape[0],
-                                                 X.shape[1], C.byref(dr), int(first), y, ldy, s),
-                   "qlora_dropout_fwd")
+    if Y is None:
+        raise ValueError("Y is missing")
+    _dropout(X, p, seed, Y, residual, first, stream, "qlora_dropout_fwd")
 
 
 def qlora_dropout_bwd(dY, p: float, seed: int, dX, first: int = 0, stream=None):
     """dX = D c dY with the forward's mask, regenerated."""
-    ldy = _rows_of(dY, "dY")
-    x, ldx = _like(dX, dY, "dX")
-    dr = _lib.Dropout(float(p), 0, int(seed))
-    with _On(dY.get_device(), stream) as s:
-        _lib.check(_lib.load().qlora_dropout_bwd(dY.data_ptr(), ldy, _float_type(dY), dY.shape[0],
-                                                 dY.shape[1], C.byref(dr), int(first), x, ldx, s),
-                   "qlora_dropout_bwd")
+    if dX is None:
+        raise ValueError("dX is missing")
+    _dropout(dY, p, seed, dX, None, first, stream, "qlora_dropout_bwd")
 
 
 def qlora_check_status(stream=None) -> int:
@@ -531,62 +607,33 @@ def mx_empty(rows: int, cols: int, device, format: int = _lib.QLORA_NVFP4) -> MX
 
 def mx_quantize(X: torch.Tensor, format: int = _lib.QLORA_NVFP4, stream=None) -> MXTensor:
     """Quantise a weight or activations: format 0 MXFP4, 1 NVFP4."""
-    _rows_of(X, "X")
-    with _On(X.get_device(), stream):
-        t = mx_empty(X.shape[0], X.shape[1], X.device, format)
-    qlora_mx_quantize(X, t, stream)
-    return t
+    return _mx_quantize(X, None, int(format), stream)
 
 
 def mx_dequantize(t: MXTensor, stream=None) -> torch.Tensor:
-    with _On(t.packed.get_device(), stream):
-        out = torch.empty((t.rows, t.cols), dtype=torch.bfloat16, device=t.packed.device)
-    qlora_mx_dequantize(t, out, stream)
-    return out
+    return _mx_dequantize(t, None, stream)
 
 
 def mx_matmul(x: MXTensor, w: MXTensor, stream=None) -> torch.Tensor:
-    with _On(x.packed.get_device(), stream):
-        Y = torch.empty((x.rows, w.rows), dtype=torch.bfloat16, device=x.packed.device)
-    qlora_mx_matmul(x, w, Y, stream)
-    return Y
+    return _mx_matmul(x, w, None, stream)
 
 
 def mx_linear_fwd(w: MXTensor, X, A=None, B=None, alpha: float = 0.0, p: float = 0.0, seed: int = 0,
                   save_T: bool = True, stream=None):
     """(Y, T) of the layer on a microscaled base; T is None without an adapter."""
-    T = None
-    with _On(X.get_device(), stream):
-        Y = torch.empty((X.shape[0], w.rows), dtype=torch.bfloat16, device=X.device)
-        if A is not None and save_T:
-            T = torch.empty((X.shape[0], A.shape[0]), dtype=torch.bfloat16, device=X.device)
-    qlora_mx_linear_fwd(w, X, A, B, alpha, Y, T, p, seed, stream=stream)
-    return Y, T
+    return _mx_fwd(w, X, A, B, alpha, None, None, save_T, p, seed, None, stream)
 
 
 def mx_linear_bwd(w: MXTensor, X, dY, A=None, B=None, alpha: float = 0.0, p: float = 0.0,
                   seed: int = 0, T=None, stream=None):
     """(dX, dA, dB); dA and dB are None without an adapter."""
-    with _On(X.get_device(), stream):
-        dX = torch.empty_like(X)
-        dA = None if A is None else torch.empty_like(A)
-        dB = None if B is None else torch.empty_like(B)
-    qlora_mx_linear_bwd(w, X, dY, A, B, alpha, dX, dA, dB, T, p, seed, stream=stream)
-    return dX, dA, dB
+    return _mx_bwd(w, X, dY, A, B, alpha, None, None, None, T, p, seed, None, stream)
 
 
 def dropout_fwd(X, p: float, seed: int, residual=None, first: int = 0, stream=None) -> torch.Tensor:
     """dropout(X) (+ residual) with the mask of the layer's dropout."""
-    _rows_of(X, "X")
-    with _On(X.get_device(), stream):
-        Y = torch.empty(X.shape, dtype=X.dtype, device=X.device)
-    qlora_dropout_fwd(X, p, seed, Y, residual, first, stream)
-    return Y
+    return _dropout(X, p, seed, None, residual, first, stream, "qlora_dropout_fwd")
 
 
 def dropout_bwd(dY, p: float, seed: int, first: int = 0, stream=None) -> torch.Tensor:
-    _rows_of(dY, "dY")
-    with _On(dY.get_device(), stream):
-        dX = torch.empty(dY.shape, dtype=dY.dtype, device=dY.device)
-    qlora_dropout_bwd(dY, p, seed, dX, first, stream)
-    return dX
+    return _dropout(dY, p, seed, None, None, first, stream, "qlora_dropout_bwd")

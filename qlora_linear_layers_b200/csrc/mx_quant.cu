@@ -85,9 +85,12 @@ __device__ __forceinline__ float mx_scale_value(uint32_t b) {
 
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// 32 consecutive elements of one row, held as loaded.
+// Consecutive elements of one row that a thread holds, 64 bytes as loaded: 32 of
+// bf16, 16 of fp32 (128 bytes a thread took 35 us for 1554 x 18944 fp32, 58 % of
+// HBM: the loads of a warp then touch a line each).
 template <typename T> struct Unit;
 template <> struct Unit<__nv_bfloat16> {
+  static constexpr int kElems = 32;
   uint4 w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
 #pragma unroll
@@ -117,14 +120,15 @@ template <> struct Unit<__nv_bfloat16> {
   }
 };
 template <> struct Unit<float> {
-  float4 w[8];
+  static constexpr int kElems = 16;
+  float4 w[4];
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < 4; ++i) w[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __device__ __forceinline__ float value(int i) const {
     const float4& v = w[i >> 2];
@@ -163,16 +167,17 @@ __device__ __forceinline__ uint2 mx_codes16(const Unit<T>& u, int h, float inv) 
 }
 
 // One row by a CTA (or by padding, live = false: zero scales only).  A thread
-// takes units of 32 elements k = tid + i * nt; with KEEP > 0 (KEEP * nt units at
-// least) the row stays in registers between NVFP4's row maximum and the codes,
-// with KEEP == 0 it is read twice.  s_max: shared, one word a warp.
+// takes units k = tid + i * nt (nt a multiple of 32); with KEEP > 0 (KEEP * nt
+// units at least) the row stays in registers between NVFP4's row maximum and the
+// codes, with KEEP == 0 it is read twice.  s_max: shared, one word a warp.
 template <typename T, int FMT, int KEEP>
 __device__ __forceinline__ void quantise_row(const T* __restrict__ x, bool live, int64_t row, int K, int tid, int nt,
                                              uint8_t* __restrict__ packed, uint8_t* __restrict__ scales,
                                              float* __restrict__ row_scale, int* status, uint32_t* s_max) {
   constexpr bool NV = FMT == QLORA_NVFP4;
-  constexpr int kGroup = NV ? 2 : 4;               // units whose scale bytes share a 32-bit word
-  const int units = K / 32;
+  constexpr int E = Unit<T>::kElems;
+  constexpr int kGroup = 4 * mx_block(FMT) / E;    // units whose scale bytes share a 32-bit word
+  const int units = K / E;
   const int upad = (units + kGroup - 1) / kGroup * kGroup;
   const int64_t tiles = mx_scale_tiles(FMT, K);
   Unit<T> u[KEEP > 0 ? KEEP : 1];
@@ -181,43 +186,46 @@ __device__ __forceinline__ void quantise_row(const T* __restrict__ x, bool live,
   auto emit = [&](int k, const Unit<T>& w) {
     const bool in = live && k < units;
     uint32_t sb = 0;                               // this unit's scale bytes, in their place of the word
-    uint4 codes;
+    uint2 c[E / 16];
     bool bad = false;
     if constexpr (NV) {
-      uint2 c[2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < E / 16; ++h) {
         const uint32_t a = w.amax16(h);
         const bool nf = a >= kInfBits;
         const uint32_t code = to_e4m3(__fdiv_rn(__fmul_rn(__uint_as_float(a), rs), 6.0f));
         c[h] = nv_codes16(w, h, rs, from_e4m3(code));
         if (nf) c[h] = make_uint2(0, 0);
         bad |= nf;
-        sb |= (nf ? 0x7Fu : code) << (8 * (2 * (k & 1) + h));
+        sb |= (nf ? 0x7Fu : code) << (8 * ((E / 16 * k + h) & 3));
       }
-      codes = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
     } else {
-      const uint32_t a = max(w.amax16(0), w.amax16(1));
+      uint32_t a = w.amax16(0);
+      if constexpr (E == 32) a = max(a, w.amax16(1));
+      else a = max(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));       // the block's other half
       const bool nf = a >= kInfBits;
       const uint32_t code = (uint32_t)max((int)(a >> 23) - 2, 0);
       const float inv = __uint_as_float((254u - code) << 23);
-      const uint2 c0 = mx_codes16(w, 0, inv), c1 = mx_codes16(w, 1, inv);
-      codes = nf ? make_uint4(0, 0, 0, 0) : make_uint4(c0.x, c0.y, c1.x, c1.y);
+#pragma unroll
+      for (int h = 0; h < E / 16; ++h) c[h] = nf ? make_uint2(0, 0) : mx_codes16(w, h, inv);
       bad |= nf;
-      sb |= (nf ? 0xFFu : code) << (8 * (k & 3));
+      const int col = E == 32 ? k : k >> 1;
+      if (E == 32 || !(k & 1)) sb = (nf ? 0xFFu : code) << (8 * (col & 3));
     }
     if (!in) sb = 0;
-    sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 1);
-    if (!NV) sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
+#pragma unroll
+    for (int o = 1; o < kGroup; o *= 2) sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, o);
     if (in) {
-      *reinterpret_cast<uint4*>(packed + row * (K / 2) + 16 * (int64_t)k) = codes;
+      uint8_t* out = packed + row * (K / 2) + E / 2 * (int64_t)k;
+      if constexpr (E == 32) *reinterpret_cast<uint4*>(out) = make_uint4(c[0].x, c[0].y, c[1].x, c[1].y);
+      else *reinterpret_cast<uint2*>(out) = c[0];
       if (bad) set_status(status, QLORA_ERR_NONFINITE);
     }
     if (k < upad && (k & (kGroup - 1)) == 0)
-      *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(row, (NV ? 2 : 1) * (int64_t)k, tiles)) = sb;
+      *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(row, (int64_t)k * E / mx_block(FMT), tiles)) = sb;
   };
   auto fetch = [&](int k, Unit<T>& w) {
-    if (live && k < units) w.load(x + 32 * (int64_t)k);
+    if (live && k < units) w.load(x + E * (int64_t)k);
     else w.zero();
   };
 
@@ -229,7 +237,7 @@ __device__ __forceinline__ void quantise_row(const T* __restrict__ x, bool live,
     uint32_t m = 0;
     auto take = [&](const Unit<T>& v) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < E / 16; ++h) {
         const uint32_t a = v.amax16(h);
         if (a < kInfBits) m = max(m, a);
       }
@@ -280,11 +288,14 @@ k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __r
 template <typename T, int FMT>
 static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int64_t ld, uint8_t* packed,
                                  uint8_t* scales, float* row_scale, int* status, cudaStream_t s) {
-  const int units = (int)(cols / 32);
-  const int upad = FMT == QLORA_NVFP4 ? (units + 1) / 2 * 2 : (units + 3) / 4 * 4;
+  constexpr int E = Unit<T>::kElems;
+  constexpr int kGroup = 4 * mx_block(FMT) / E;
+  const int units = (int)(cols / E);
+  const int upad = (units + kGroup - 1) / kGroup * kGroup;
   const int64_t prow = (rows + 127) / 128 * 128;
   auto run = [&](auto kern, int per) {
-    const int nt = std::min(512, std::max(32, ((upad + per - 1) / per + 31) / 32 * 32));
+    const int rounds = std::max(per, (upad + 511) / 512);          // equal rounds of at most 512 threads
+    const int nt = std::max(32, ((upad + rounds - 1) / rounds + 31) / 32 * 32);
     kern<<<(unsigned)prow, nt, 0, s>>>((const T*)X, ld, (int)rows, (int)cols, packed, scales, row_scale, status);
   };
   if (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);

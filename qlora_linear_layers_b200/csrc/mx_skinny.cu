@@ -12,7 +12,9 @@
 // the GPU, and adds the partial sums through distributed shared memory in rank
 // order: one launch, no workspace, the same bits every time.
 //
-//  * warp 0: TMA (a stage: 64 of the contraction, 16 KB + up to 16 KB);
+//  * warp 0: TMA (a stage: 64 of the contraction, 16 KB + 2 to 16 KB), as many
+//    stages as fit, since the bytes in flight are what the read's rate needs:
+//    with three stages a CTA took 0.33 us a stage, 54 GB/s;
 //  * warp 1: tcgen05.mma kind::f16, M = 128, N = r (at least 16);
 //  * warps 2-5: cluster reduction, rounding, stores.
 // Every wait is bounded (QLORA_ERR_TIMEOUT).
@@ -33,9 +35,9 @@ namespace skinny {
 
 using mx::elect_one;
 
-constexpr int NS = 3;
 constexpr int NUM_THREADS = 192;
-constexpr int A_BYTES = 128 * 64 * 2, B_BYTES = 128 * 64 * 2;    // B at its largest
+constexpr int kMaxStages = 10;
+constexpr int A_BYTES = 128 * 64 * 2;
 
 // One product of a launch (an outer launch has up to two).
 struct Problem {
@@ -52,19 +54,18 @@ struct Args {
   int L;                    // contraction length
   int r, N, RP;             // rank; MMA N (a power of two, 16 to 128); padded width
   int log_splits;
+  int ns, b_bytes;          // stages and the bytes of B in one
   int* status;
 };
 
-struct Smem {
-  uint8_t a[NS][A_BYTES];   // a, then b: the partial sums of the reduction
-  uint8_t b[NS][B_BYTES];
-  uint64_t full[NS], empty[NS], acc_full;
+// Shared memory: this, then ns stages of A and B, 1024-byte aligned; the
+// reduction's partial sums (N * 512 bytes) take the stages' place.
+struct Head {
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
   uint32_t tmem_base;
   int abort;
 };
-constexpr size_t kSmemBytes = sizeof(Smem) + 1024;
-static_assert(2 * (kSmemBytes + 1024) <= 228 * 1024, "two CTAs an SM");
-static_assert(128 * 128 * 4 <= NS * (A_BYTES + B_BYTES), "reduction buffer");
+static_assert(sizeof(Head) <= 1024, "stages begin at 1024");
 
 // MN-major operand with a 128-byte swizzle: 64 consecutive elements of a row are
 // 128 bytes, eight rows 1024 bytes (the stride between groups of the
@@ -79,13 +80,69 @@ __device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t group) {
   return d;
 }
 
+// Two results of a row, columns col and col + 1.
+template <bool OUTER>
+__device__ __forceinline__ void store2(const Args& g, const Problem& p, const float* v, int row, int col) {
+  if (row >= p.rows) return;
+  if (OUTER) {
+    if (col >= g.r) return;
+    if (p.transposed) {
+      p.out[(int64_t)col * p.rows + row] = __float2bfloat16_rn(__fmul_rn(p.s, v[0]));
+      p.out[(int64_t)(col + 1) * p.rows + row] = __float2bfloat16_rn(__fmul_rn(p.s, v[1]));
+    } else {
+      *reinterpret_cast<uint32_t*>(p.out + (int64_t)row * g.r + col) =
+          pack_bf16x2(__fmul_rn(p.s, v[0]), __fmul_rn(p.s, v[1]));
+    }
+  } else {
+    float a = __fmul_rn(p.s, v[0]), b = __fmul_rn(p.s, v[1]);
+    if (p.row_scale) {
+      const float d = p.row_scale[row];
+      a = __fdiv_rn(a, d);
+      b = __fdiv_rn(b, d);
+    }
+    if (p.pad) *reinterpret_cast<uint32_t*>(p.pad + (int64_t)row * g.RP + col) = pack_bf16x2(a, b);
+    if (p.out && col < g.r) *reinterpret_cast<uint32_t*>(p.out + (int64_t)row * g.r + col) = pack_bf16x2(v[0], v[1]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// Eight, columns col .. col + 7 (col a multiple of 8, like r).
+template <bool OUTER>
+__device__ __forceinline__ void store8(const Args& g, const Problem& p, const float* v, int row, int col) {
+  if (row >= p.rows) return;
+  if (OUTER && p.transposed) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) store2<OUTER>(g, p, v + j, row, col + j);
+    return;
+  }
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(p.s, v[j]);
+  if (OUTER) {
+    if (col < g.r) *reinterpret_cast<uint4*>(p.out + (int64_t)row * g.r + col) = pack8(f);
+    return;
+  }
+  if (p.row_scale) {
+    const float d = p.row_scale[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], d);
+  }
+  if (p.pad) *reinterpret_cast<uint4*>(p.pad + (int64_t)row * g.RP + col) = pack8(f);
+  if (p.out && col < g.r) *reinterpret_cast<uint4*>(p.out + (int64_t)row * g.r + col) = pack8(v);
+}
+
 template <bool OUTER>
 __global__ void __launch_bounds__(NUM_THREADS, 2)
 k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
             const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
             const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
-  Smem& S = *smem_align1024<Smem>(smem_raw);
+  Head& S = *smem_align1024<Head>(smem_raw);
+  uint8_t* stages = reinterpret_cast<uint8_t*>(&S) + 1024;
+  const int NS = g.ns, stage_bytes = A_BYTES + g.b_bytes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ls = g.log_splits, splits = 1 << ls;
   const int rank = (int)cluster_ctarank();
@@ -124,20 +181,20 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 
   if (warp == 0) {
     if (elect_one()) {
-      const int b_boxes = OUTER ? (g.N + 63) / 64 : 1;
-      const uint32_t bytes = A_BYTES + (OUTER ? b_boxes * 8192 : g.N * 128);
       int s = 0, i = k0;
       uint32_t ph = 0;
       for (; i < k1; ++i) {
         if (!mbar_wait(&S.empty[s], ph ^ 1, abort, g.status)) break;
-        mbar_arrive_expect_tx(&S.full[s], bytes);
+        mbar_arrive_expect_tx(&S.full[s], stage_bytes);
+        uint8_t* a = stages + s * stage_bytes;
+        uint8_t* b = a + A_BYTES;
         if (OUTER) {
-          tma_load_2d(S.a[s], tm_a, &S.full[s], row0, i * 64);
-          tma_load_2d(S.a[s] + 8192, tm_a, &S.full[s], row0 + 64, i * 64);
-          for (int b = 0; b < b_boxes; ++b) tma_load_2d(S.b[s] + b * 8192, tm_b, &S.full[s], b * 64, i * 64);
+          tma_load_2d(a, tm_a, &S.full[s], row0, i * 64);
+          tma_load_2d(a + 8192, tm_a, &S.full[s], row0 + 64, i * 64);
+          for (int j = 0; j * 8192 < g.b_bytes; ++j) tma_load_2d(b + j * 8192, tm_b, &S.full[s], j * 64, i * 64);
         } else {
-          tma_load_2d(S.a[s], tm_a, &S.full[s], i * 64, row0);
-          tma_load_2d(S.b[s], tm_b, &S.full[s], i * 64, 0);
+          tma_load_2d(a, tm_a, &S.full[s], i * 64, row0);
+          tma_load_2d(b, tm_b, &S.full[s], i * 64, 0);
         }
         if (++s == NS) { s = 0; ph ^= 1; }
       }
@@ -155,7 +212,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
       for (int i = k0; i < k1; ++i) {
         if (!mbar_wait(&S.full[s], ph, abort, g.status)) break;
         tc_fence_after();
-        const uint32_t aa = smem_u32(S.a[s]), bb = smem_u32(S.b[s]);
+        const uint32_t aa = smem_u32(stages + s * stage_bytes), bb = aa + A_BYTES;
         const uint64_t a = OUTER ? mn_desc(aa, 8192) : sw128_kmajor_desc(aa);
         const uint64_t b = OUTER ? mn_desc(bb, 8192) : sw128_kmajor_desc(bb);
         constexpr uint32_t kStep = OUTER ? 2048 / 16 : 32 / 16;  // 16 rows, or 16 elements of a row
@@ -171,58 +228,68 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     mbar_wait(&S.acc_full, 0, abort, g.status);
   }
   __syncwarp();
-  cluster_sync();                                  // every rank is done with its stages
   const int quad = warp & 3;
   const int at = quad * 32 + lane, row = row0 + at;
-  const int cs = g.N >> ls, lcs = __ffs(cs) - 1;   // columns each rank adds up (even)
-  float* part = reinterpret_cast<float*>(S.a[0]);  // [splits][cs][128]
-  if (warp >= 2) {
-    tc_fence_after();
+  const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16);
+  if (ls == 0) {
+    if (warp >= 2) {
+      tc_fence_after();
 #pragma unroll 1
-    for (int c = 0; c < g.N; c += 16) {
-      uint32_t v[16];
-      tmem_ld16(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
-      tmem_wait_ld();
-      const uint32_t mine = smem_u32(part + rank * cs * 128 + at);
-#pragma unroll
-      for (int j = 0; j < 16; ++j)
-        mx::st_cluster_f32(mapa_shared(mine + (uint32_t)(((c + j) & (cs - 1)) * 512), (c + j) >> lcs),
-                           __uint_as_float(v[j]));
-    }
-  }
-  cluster_sync();                                  // the partial sums have arrived
-  if (warp >= 2 && row < p.rows) {
-    const int col0 = rank * cs;
-    const float f = OUTER ? p.s : 1.0f;
-    const float div = !OUTER && p.row_scale ? p.row_scale[row] : 1.0f;
-    for (int c = 0; c < cs; c += 2) {
-      float v[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float* b = part + (c + j) * 128 + at;
-        v[j] = b[0];
-        for (int z = 1; z < splits; ++z) v[j] = __fadd_rn(v[j], b[z * cs * 128]);
+      for (int c = 0; c < g.N; c += 16) {
+        float v[16];
+        tmem_ld16(taddr + c, reinterpret_cast<uint32_t*>(v));
+        tmem_wait_ld();
+        store8<OUTER>(g, p, v, row, c);
+        store8<OUTER>(g, p, v + 8, row, c + 8);
       }
-      const int col = col0 + c;
-      if (OUTER) {
-        if (col >= g.r) break;
-        if (p.transposed) {
-          p.out[(int64_t)col * p.rows + row] = __float2bfloat16_rn(__fmul_rn(f, v[0]));
-          p.out[(int64_t)(col + 1) * p.rows + row] = __float2bfloat16_rn(__fmul_rn(f, v[1]));
-        } else {
-          *reinterpret_cast<uint32_t*>(p.out + (int64_t)row * g.r + col) =
-              pack_bf16x2(__fmul_rn(f, v[0]), __fmul_rn(f, v[1]));
+    }
+  } else {
+    cluster_sync();                                // every rank is done with its stages
+    const int cs = g.N >> ls, lcs = __ffs(cs) - 1; // columns each rank adds up (a power of two)
+    float* part = reinterpret_cast<float*>(stages);  // [splits][cs][128]
+    if (warp >= 2) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < g.N; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(taddr + c, v);
+        tmem_wait_ld();
+        const uint32_t mine = smem_u32(part + rank * cs * 128 + at);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          mx::st_cluster_f32(mapa_shared(mine + (uint32_t)(((c + j) & (cs - 1)) * 512), (c + j) >> lcs),
+                             __uint_as_float(v[j]));
+      }
+    }
+    cluster_sync();                                // the partial sums have arrived
+    if (warp >= 2) {
+      const float* b = part + at;
+      if (cs >= 8) {
+#pragma unroll 1
+        for (int c = 0; c < cs; c += 8) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = b[(c + j) * 128];
+          for (int z = 1; z < splits; ++z)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(v[j], b[(z * cs + c + j) * 128]);
+          store8<OUTER>(g, p, v, row, rank * cs + c);
         }
       } else {
-        float a = __fmul_rn(p.s, v[0]), b = __fmul_rn(p.s, v[1]);
-        if (p.row_scale) { a = __fdiv_rn(a, div); b = __fdiv_rn(b, div); }
-        if (p.pad) *reinterpret_cast<uint32_t*>(p.pad + (int64_t)row * g.RP + col) = pack_bf16x2(a, b);
-        if (p.out && col < g.r) *reinterpret_cast<uint32_t*>(p.out + (int64_t)row * g.r + col) = pack_bf16x2(v[0], v[1]);
+        for (int c = 0; c < cs; c += 2) {          // 2 or 4 columns
+          float v[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            v[j] = b[(c + j) * 128];
+            for (int z = 1; z < splits; ++z) v[j] = __fadd_rn(v[j], b[(z * cs + c + j) * 128]);
+          }
+          store2<OUTER>(g, p, v, row, rank * cs + c);
+        }
       }
     }
-    if (!OUTER && p.pad && rank == 0)
-      for (int c = g.N; c < g.RP; c += 8) *reinterpret_cast<uint4*>(p.pad + (int64_t)row * g.RP + c) = make_uint4(0, 0, 0, 0);
   }
+  if (!OUTER && warp >= 2 && rank == 0 && p.pad && row < p.rows)
+    for (int c = g.N; c < g.RP; c += 8) *reinterpret_cast<uint4*>(p.pad + (int64_t)row * g.RP + c) = make_uint4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -231,23 +298,28 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   }
 }
 
-// Ranks of a cluster: up to about two CTAs an SM, at least four stages each.
-static int log_splits_of(int tiles, int L, int num_sms) {
-  const int nk = (L + 63) / 64;
+// Ranks of a cluster and stages: up to one CTA an SM, of at least four stages
+// each, with all of its shared memory; with more tiles than SMs two CTAs share
+// one.  8192 x 4096, r = 64 (64 tiles): 15 us with 2 ranks and 8 stages against
+// 29 us unsplit and 20.5 us with 4 ranks, two CTAs an SM of 3 stages.
+static void shape(Args& g, int num_sms) {
+  const int tiles = g.p[0].tiles + g.p[1].tiles, nk = (g.L + 63) / 64;
   int ls = 0;
-  while (ls < 3 && (tiles << (ls + 1)) <= 2 * num_sms && (nk >> (ls + 1)) >= 4) ++ls;
-  return ls;
+  while (ls < 3 && (tiles << (ls + 1)) <= num_sms && (nk >> (ls + 1)) >= 4) ++ls;
+  g.log_splits = ls;
+  const int budget = ((tiles << ls) > num_sms ? 110 : 224) * 1024 - 2048;
+  g.ns = std::min(kMaxStages, budget / (A_BYTES + g.b_bytes));
 }
 
 template <bool OUTER>
 static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
                   const Args& g, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_devs{0};
-  set_smem_attr_once(k_mx_skinny<OUTER>, (int)kSmemBytes, attr_devs);
+  set_smem_attr_once(k_mx_skinny<OUTER>, 224 * 1024, attr_devs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(g.p[0].tiles + g.p[1].tiles) << g.log_splits, 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = 2048 + (size_t)g.ns * (A_BYTES + g.b_bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -271,7 +343,8 @@ int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, fl
   g.RP = RP;
   g.status = status;
   g.p[0] = Problem{M, (M + 127) / 128, row_scale, (__nv_bfloat16*)pad, (__nv_bfloat16*)out, 0, s};
-  g.log_splits = log_splits_of(g.p[0].tiles, L, num_sms);
+  g.b_bytes = g.N * 128;
+  shape(g, num_sms);
   CUtensorMap a, b;
   if (!make_tmap_2d_bf16(&a, Z, L, M, L, 64, 128) || !make_tmap_2d_bf16(&b, R, L, r, L, 64, g.N)) return QLORA_ERR_CUDA;
   return launch<false>(a, b, a, b, g, st);
@@ -287,7 +360,8 @@ int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, co
   g.status = status;
   g.p[0] = Problem{K, (K + 127) / 128, nullptr, nullptr, (__nv_bfloat16*)dA, 1, 1.0f};
   g.p[1] = Problem{N, (N + 127) / 128, nullptr, nullptr, (__nv_bfloat16*)dB, 0, s};
-  g.log_splits = log_splits_of(g.p[0].tiles + g.p[1].tiles, M, num_sms);
+  g.b_bytes = (g.N + 63) / 64 * 8192;
+  shape(g, num_sms);
   CUtensorMap a0, b0, a1, b1;
   if (!make_tmap_2d_bf16(&a0, Xd, K, M, K, 64, 64) || !make_tmap_2d_bf16(&b0, sU, r, M, ldu, 64, 64) ||
       !make_tmap_2d_bf16(&a1, dY, N, M, N, 64, 64) || !make_tmap_2d_bf16(&b1, T, r, M, r, 64, 64))
@@ -298,35 +372,51 @@ int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, co
 // ===========================================================================
 // The backward's transposed adapter factors, in one launch:
 //   At[K, RP] = A[r, K]^T, zero beyond r     Bt[r, N] = B[N, r]^T
-// Tiles of 64 x r through shared memory (a row of 64 or r elements at a time).
+// A CTA a tile of 64 columns of A or rows of B, through shared memory; 16-byte
+// words of global memory on both sides, single elements in shared memory.
 // ===========================================================================
 __global__ void __launch_bounds__(256)
 k_mx_transpose(const __nv_bfloat16* __restrict__ A, const __nv_bfloat16* __restrict__ B, int r, int K, int N, int RP,
                __nv_bfloat16* __restrict__ At, __nv_bfloat16* __restrict__ Bt) {
-  __shared__ __nv_bfloat16 tile[64][130];
+  __shared__ uint16_t tile[64][130];               // [column of A or row of B][row of A or column of B]
   const int ka = (K + 63) / 64;
   const int tid = threadIdx.x;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
   if ((int)blockIdx.x < ka) {
     const int k0 = blockIdx.x * 64;
-    for (int i = tid; i < r * 64; i += 256) {
-      const int j = i >> 6, k = i & 63;
-      tile[k][j] = k0 + k < K ? A[(int64_t)j * K + k0 + k] : __nv_bfloat16();
+    for (int i = tid; i < RP * 8; i += 256) {
+      const int j = i >> 3, k = 8 * (i & 7);
+      const uint4 v = j < r && k0 + k < K ? *reinterpret_cast<const uint4*>(A + (int64_t)j * K + k0 + k) : zero;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tile[k + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
     __syncthreads();
-    for (int i = tid; i < 64 * RP; i += 256) {
-      const int k = i / RP, j = i % RP;
-      if (k0 + k < K) At[(int64_t)(k0 + k) * RP + j] = j < r ? tile[k][j] : __float2bfloat16_rn(0.0f);
+    for (int i = tid; i < 64 * (RP / 8); i += 256) {
+      const int k = i / (RP / 8), j = 8 * (i % (RP / 8));
+      if (k0 + k >= K) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = tile[k][j + 2 * e] | (uint32_t)tile[k][j + 2 * e + 1] << 16;
+      *reinterpret_cast<uint4*>(At + (int64_t)(k0 + k) * RP + j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   } else {
     const int n0 = ((int)blockIdx.x - ka) * 64;
-    for (int i = tid; i < r * 64; i += 256) {
-      const int n = i / r, j = i % r;
-      tile[n][j] = n0 + n < N ? B[(int64_t)(n0 + n) * r + j] : __nv_bfloat16();
+    for (int i = tid; i < 64 * (r / 8); i += 256) {
+      const int n = i / (r / 8), j = 8 * (i % (r / 8));
+      const uint4 v = n0 + n < N ? *reinterpret_cast<const uint4*>(B + (int64_t)(n0 + n) * r + j) : zero;
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tile[n][j + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
     __syncthreads();
-    for (int i = tid; i < r * 64; i += 256) {
-      const int j = i >> 6, n = i & 63;
-      if (n0 + n < N) Bt[(int64_t)j * N + n0 + n] = tile[n][j];
+    for (int i = tid; i < r * 8; i += 256) {
+      const int j = i >> 3, n = 8 * (i & 7);
+      if (n0 + n >= N) continue;                   // N % 8 == 0
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = tile[n + 2 * e][j] | (uint32_t)tile[n + 2 * e + 1][j] << 16;
+      *reinterpret_cast<uint4*>(Bt + (int64_t)j * N + n0 + n) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
