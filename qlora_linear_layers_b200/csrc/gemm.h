@@ -61,6 +61,9 @@ size_t gemv_workspace_bytes(int M, int N, int K, int r);
 // 2-D bf16 tensor map, 128-byte swizzle, box [box_outer rows x box_inner cols].
 bool make_tmap_2d_bf16(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,
                        uint64_t row_stride_elems, uint32_t box_inner, uint32_t box_outer);
+// bf16 matrix [outer, inner] to store to, 64-byte swizzle, box [box_outer rows x
+// 32 columns]; inner a multiple of 8.
+bool make_tmap_store_bf16(CUtensorMap* tm, void* base, uint64_t inner, uint64_t outer, uint32_t box_outer);
 // Same for a uint8 matrix: inner extent and row stride in bytes; 128-byte
 // swizzle (box_inner <= 128) or none.
 bool make_tmap_2d_u8(CUtensorMap* tm, const void* base, uint64_t inner, uint64_t outer,

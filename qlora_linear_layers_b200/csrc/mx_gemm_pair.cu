@@ -18,7 +18,10 @@
 //    wait of a stage;
 //  * one accumulator: eight epilogue warps take it to registers as it is (128
 //    values a thread), hand it back, and scale, round and store under the next
-//    tile's MMAs.  Two accumulators would hide that read too, but with tiles of
+//    tile's MMAs.  They read it in the fragments that stmatrix transposes, so a
+//    token's 32 outputs leave shared memory by TMA; stored from registers, a
+//    4-byte word a lane, a tile's epilogue was longer than its MMAs (8192 x 18944
+//    x 3584 NVFP4: 220 us against 181 us without stores).  Two accumulators would hide that read too, but with tiles of
 //    192 tokens, whose MMAs do 8 % less per cycle.
 // The adapter's bf16 K steps (kind::f16) come first and are complete before the
 // block-scaled MMAs of the tile begin: MMAs of two kinds need not run in order.
@@ -45,6 +48,38 @@ namespace mx {
 constexpr int P_EPI = 8;                           // epilogue warps
 constexpr int P_THREADS = 64 + 32 * P_EPI;         // warp 0 TMA, 1 MMA, 2-9 epilogue
 constexpr uint16_t kBoth = 0x3;
+constexpr int kChunk = 32;                         // tokens of an output chunk
+
+// Warp-wide: 16 lanes x 32 columns of tensor memory; of every 8 columns thread t
+// gets columns 2 (t % 4), + 1 of lane t / 4 (v[4 j], v[4 j + 1]) and of lane
+// t / 4 + 8 (v[4 j + 2], v[4 j + 3]).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 bf16 blocks of a warp, transposed: row i of block j goes to the
+// address that lane 8 j + i holds.
+__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+               :: "r"(addr), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+               :: "l"(tmap), "r"(smem_u32(smem_src)), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
+}
+
 
 template <int FMT, int PN>
 struct PairShape {
@@ -66,6 +101,7 @@ struct PairSmem {
   uint8_t x[Sh::NS][Sh::X_BYTES];
   uint8_t sw[Sh::NS][Sh::SW_BYTES];
   uint8_t sx[Sh::NS][Sh::SX_BYTES];
+  uint8_t out[P_EPI][2][kChunk * 64];              // a warp's chunks of kChunk tokens x 32 outputs
   float rx[2][PN];
   uint64_t full[Sh::NS], empty[Sh::NS], acc_full, acc_empty, kind, done;
   uint32_t tmem_base;
@@ -77,7 +113,7 @@ __global__ void __launch_bounds__(P_THREADS, 1)
 k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_sx,
                const __grid_constant__ CUtensorMap tm_wad, const __grid_constant__ CUtensorMap tm_xad,
-               const Args p) {
+               const __grid_constant__ CUtensorMap tm_out, const Args p) {
   using Sh = PairShape<FMT, PN>;
   constexpr int NS = Sh::NS, NT = Sh::NT, RB = Sh::RB, PNH = Sh::PNH;
   constexpr bool NV = FMT == QLORA_NVFP4;
@@ -208,16 +244,21 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     constexpr int HC = PN / 2;
     const int quad = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16) + half * HC;
-    const bool odd = lane & 1;
-    const bool pairs = (p.N & 1) == 0;
+    const bool whole = (p.N & 7) == 0;             // rows of Y that TMA can store to
+    const int e = warp - 2;
+    const int g = lane >> 2;                       // fragment row
     const uint32_t acc_empty0 = mapa_shared(smem_u32(&S.acc_empty), 0);
+    // this lane's row of the four blocks of a stmatrix: token lane % 8, outputs 8 (lane / 8) ..
+    const uint32_t row_off = (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
     uint32_t tp = 0;
     for (int tile = cluster; tile < n_tiles; tile += n_clusters, tp ^= 1) {
-      const int n = (tile % tiles_n) * (2 * BW) + (int)rank * BW + quad * 32 + lane;
+      const int nw = (tile % tiles_n) * (2 * BW) + (int)rank * BW + quad * 32;     // the warp's outputs
       const int mt = (tile / tiles_n) * PN, m0 = mt + half * HC;
-      float rw = 1.0f;
+      float rw[4] = {1.0f, 1.0f, 1.0f, 1.0f};
       if (NV) {
-        if (n < p.N) rw = p.wr[n];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (nw + 8 * i + g < p.N) rw[i] = p.wr[nw + 8 * i + g];
         // the readers of this buffer, two tiles ago, passed the last tile's barrier
         for (int i = threadIdx.x - 64; i < PN; i += 32 * P_EPI) S.rx[tp][i] = mt + i < p.M ? p.xr[mt + i] : 0.0f;
         asm volatile("bar.sync 1, %0;" :: "n"(32 * P_EPI) : "memory");
@@ -225,20 +266,59 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       if (!mbar_wait_cluster(&S.acc_full, tp, abort, p.status)) break;
       __syncwarp();
       tc_fence_after();
-      uint32_t v[HC];
+      uint32_t v[HC / 32][2][16];
 #pragma unroll
-      for (int c = 0; c < HC; c += 32) tmem_ld32(taddr + c, v + c);
+      for (int c = 0; c < HC / 32; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) tmem_ld_16x32(taddr + 32 * c + ((uint32_t)(16 * h) << 16), v[c][h]);
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acc_empty0);
-      if (NV) {
 #pragma unroll
-        for (int j = 0; j < HC; ++j)
-          v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(S.rx[tp][half * HC + j], rw)));
+      for (int c = 0; c < HC / 32; ++c) {
+        const int m = m0 + 32 * c;
+        if (m >= p.M || nw >= p.N) break;
+        uint8_t* out = S.out[e][c & 1];
+        if (lane == 0) store_wait_read<1>();       // the store before the last one has left its chunk
+        __syncwarp();
+        const uint32_t to = smem_u32(out) + row_off;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {              // tokens 8 j .. 8 j + 7
+          uint32_t o[4];                           // outputs 8 i .. 8 i + 7
+          float2 rx = make_float2(1.0f, 1.0f);
+          if (NV) rx = *reinterpret_cast<const float2*>(&S.rx[tp][half * HC + 32 * c + 8 * j + 2 * (lane & 3)]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a = __uint_as_float(v[c][i >> 1][4 * j + 2 * (i & 1)]);
+            float b = __uint_as_float(v[c][i >> 1][4 * j + 2 * (i & 1) + 1]);
+            if (NV) {
+              a = __fmul_rn(a, __fmul_rn(rx.x, rw[i]));
+              b = __fmul_rn(b, __fmul_rn(rx.y, rw[i]));
+            }
+            o[i] = pack_bf16x2(a, b);
+          }
+          stmatrix_x4_t(to + 512 * j, o[0], o[1], o[2], o[3]);
+        }
+        if (whole) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tm_out, out, nw, m);
+            store_commit();
+          }
+        } else {                                   // rows of Y without 16-byte boundaries
+          __syncwarp();
+          const int t = lane;                      // a token a lane
+          if (m + t < p.M)
+            for (int i = 0; i < 32 && nw + i < p.N; ++i)
+              p.out[(int64_t)(m + t) * p.N + nw + i] = *reinterpret_cast<const __nv_bfloat16*>(
+                  out + t * 64 + (((i >> 3) ^ ((t >> 1) & 3)) << 4) + (i & 7) * 2);
+          __syncwarp();
+        }
       }
-      store_columns<HC>(p, v, m0, n, n - (odd ? 1 : 0), odd, pairs);
     }
+    if (lane == 0) store_wait_read<0>();           // the chunks outlive the stores that read them
   }
 
   if (warp == 0 && lane == 0 && *abort) {
@@ -282,7 +362,7 @@ template <int FMT, int PN>
 static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
                        cudaStream_t s, int num_sms) {
   using Sh = PairShape<FMT, PN>;
-  CUtensorMap tw, tx, tsw, tsx, twa, txa;
+  CUtensorMap tw, tx, tsw, tsx, twa, txa, to;
   const uint64_t kb = (uint64_t)a.K / 2;
   if (!make_tmap_2d_u8(&tw, w->packed, kb, a.N, kb, BKB, BW, true) ||
       !make_tmap_2d_u8(&tx, x->packed, kb, a.M, kb, BKB, Sh::PNH, true) ||
@@ -291,6 +371,8 @@ static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const
     return QLORA_ERR_CUDA;
   twa = tw;
   txa = tx;
+  to = tw;
+  if (a.N % 8 == 0 && !make_tmap_store_bf16(&to, a.out, a.N, a.M, kChunk)) return QLORA_ERR_CUDA;
   if (ad.RP && (!make_tmap_2d_bf16(&twa, ad.wt, ad.RP, a.N, ad.RP, 64, BW) ||
                 !make_tmap_2d_bf16(&txa, ad.tok, ad.RP, a.M, ad.RP, 64, Sh::PNH)))
     return QLORA_ERR_CUDA;
@@ -311,7 +393,7 @@ static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_mx_gemm_pair<FMT, PN>, tw, tx, tsw, tsx, twa, txa, a) == cudaSuccess
+  return cudaLaunchKernelEx(&cfg, k_mx_gemm_pair<FMT, PN>, tw, tx, tsw, tsx, twa, txa, to, a) == cudaSuccess
              ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
