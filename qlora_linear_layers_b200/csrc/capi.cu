@@ -847,7 +847,7 @@ int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY,
   if (e1) cudaEventRecord(e1, s);
   if (st) return st;
   if (dr.on) {
-    launch_rank_add(sU, RP, A, r, (int)M, (int)K, dX, dr, s);
+    launch_mx_rank_add(sU, At, RP, (int)M, (int)K, dX, dr, s);
     ++n;
   }
   if (r) {

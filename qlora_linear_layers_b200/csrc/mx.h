@@ -25,6 +25,11 @@ __host__ __device__ constexpr int64_t mx_scale_offset(int64_t r, int64_t c, int6
 void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
                         uint8_t* packed, uint8_t* scales, float* row_scale, int* status,
                         cudaStream_t s);
+struct Dropout;
+// dX [M, K] (bf16, in place) += D c (sU [M, RP] At [K, RP]^T), K % 64 == 0.
+void launch_mx_rank_add(const void* sU, const void* At, int RP, int M, int K, void* dX, const Dropout& drop,
+                        cudaStream_t s);
+
 // Few tokens (M <= kMxFewTokens): X [M, K] bf16 quantised (scales of rows past M
 // are left as they are) and, with r > 0 and T = X A^T, sT [M, r] = RNbf16(s T)
 // and T_save = RNbf16(T) (may be null).  K <= kMxPrepMaxK.

@@ -460,45 +460,57 @@ void launch_mx_dequantize(const qlora_mx_tensor* t, void* out, cudaStream_t s) {
 }
 
 // ===========================================================================
-// Dequantise-transpose for the backward's dX: CTA tile 64 rows (n) x 128
-// columns (k).  Thread (pr, qk) expands rows 2 pr, 2 pr + 1, columns
-// [16 qk, 16 qk + 16) -- within one block of either format -- and stores each
-// column's pair of rows as one word of the transposed tile in shared memory (a
-// warp's words are consecutive); the tile leaves in 16-byte stores.
+// Dequantise-transpose for the backward's dX: CTA tile 64 rows (n) x 256 columns
+// (k), bound by the 2-byte stores.  Thread (pr, qk) expands rows 2 pr, 2 pr + 1,
+// columns [32 qk, 32 qk + 32) from 16-byte words and stores each column's pair of
+// rows as one word of the transposed tile in shared memory (a warp's words are
+// consecutive); the tile leaves in 16-byte stores, 128 bytes a row.
 // ===========================================================================
 template <int FMT>
 __global__ void __launch_bounds__(256)
 k_mx_dequant_t(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ scales,
                const float* __restrict__ row_scale, int N, int K, __nv_bfloat16* __restrict__ Wt) {
   constexpr int kPitch = 36;                       // words per transposed row (32 + pad, 16-byte rows)
-  __shared__ __align__(16) uint32_t tileT[128 * kPitch];
-  const int n0 = blockIdx.y * 64, k0 = blockIdx.x * 128;
+  __shared__ __align__(16) uint32_t tileT[256 * kPitch];
+  const int n0 = blockIdx.y * 64, k0 = blockIdx.x * 256;
   const int tid = threadIdx.x;
   const int pr = tid & 31, qk = tid >> 5;
-  const int k = k0 + 16 * qk;
+  const int k = k0 + 32 * qk;
   const int64_t tiles = mx_scale_tiles(FMT, K);
-  uint32_t v[2][8];                                // bf16 pairs of the two rows
+  uint4 cw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  float S[2][2] = {}, rs[2] = {1.0f, 1.0f};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int n = n0 + 2 * pr + h;
-    uint4 a = make_uint4(0, 0, 0, 0), b = a;
-    if (k < K && n < N) {
-      const uint2 cw = *reinterpret_cast<const uint2*>(packed + ((int64_t)n * K + k) / 2);
-      const float S = mx_scale_value<FMT>(scales[mx_scale_offset(n, k / mx_block(FMT), tiles)]);
-      const float rs = FMT == QLORA_NVFP4 ? row_scale[n] : 1.0f;
-      a = mx_values8<FMT>(cw.x, S, rs);
-      b = mx_values8<FMT>(cw.y, S, rs);
+    if (k < K && n < N) {                          // K % 32 == 0: 32 columns or none
+      cw[h] = __ldg(reinterpret_cast<const uint4*>(packed + ((int64_t)n * K + k) / 2));
+      if (FMT == QLORA_NVFP4) {
+        const uint32_t b = *reinterpret_cast<const uint16_t*>(scales + mx_scale_offset(n, k / 16, tiles));
+        S[h][0] = from_e4m3(b & 0xFFu);
+        S[h][1] = from_e4m3(b >> 8);
+        rs[h] = row_scale[n];
+      } else {
+        S[h][0] = S[h][1] = from_e8m0(scales[mx_scale_offset(n, k / 32, tiles)]);
+      }
     }
-    v[h][0] = a.x; v[h][1] = a.y; v[h][2] = a.z; v[h][3] = a.w;
-    v[h][4] = b.x; v[h][5] = b.y; v[h][6] = b.z; v[h][7] = b.w;
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    tileT[(16 * qk + 2 * j) * kPitch + pr] = prmt(v[0][j], v[1][j], 0x5410);
-    tileT[(16 * qk + 2 * j + 1) * kPitch + pr] = prmt(v[0][j], v[1][j], 0x7632);
+  for (int q = 0; q < 4; ++q) {
+    uint4 v[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      v[h] = mx_values8<FMT>(q == 0 ? cw[h].x : q == 1 ? cw[h].y : q == 2 ? cw[h].z : cw[h].w, S[h][q >> 1], rs[h]);
+    const uint32_t a[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, b[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t* t = tileT + (32 * qk + 8 * q + 2 * j) * kPitch + pr;
+      t[0] = prmt(a[j], b[j], 0x5410);
+      t[kPitch] = prmt(a[j], b[j], 0x7632);
+    }
   }
   __syncthreads();
-  for (int i = tid; i < 128 * 8; i += 256) {
+#pragma unroll 4
+  for (int i = tid; i < 256 * 8; i += 256) {
     const int kr = i >> 3, ch = i & 7;             // transposed row, 16-byte chunk (8 columns n)
     const int kk = k0 + kr, nn = n0 + ch * 8;
     if (kk < K && nn < N)                          // N % 8 == 0: a chunk is whole
@@ -508,7 +520,7 @@ k_mx_dequant_t(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ s
 }
 
 void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s) {
-  const dim3 grid((unsigned)((w->cols + 127) / 128), (unsigned)((w->rows + 63) / 64));
+  const dim3 grid((unsigned)((w->cols + 255) / 256), (unsigned)((w->rows + 63) / 64));
   auto run = [&](auto kern) {
     kern<<<grid, 256, 0, s>>>(w->packed, w->scales, w->row_scale, (int)w->rows, (int)w->cols, (__nv_bfloat16*)Wt);
   };

@@ -29,6 +29,8 @@
 #include "gemm.h"
 #include "mx.h"
 #include "mx_gemm.cuh"
+#include "mx_mma.cuh"
+#include "draw.cuh"
 
 namespace qnf4 {
 namespace skinny {
@@ -425,6 +427,71 @@ void launch_mx_transpose(const void* A, const void* B, int r, int K, int N, int 
                          cudaStream_t s) {
   k_mx_transpose<<<(K + 63) / 64 + (N + 63) / 64, 256, 0, s>>>((const __nv_bfloat16*)A, (const __nv_bfloat16*)B, r, K, N,
                                                                RP, (__nv_bfloat16*)At, (__nv_bfloat16*)Bt);
+}
+
+// ===========================================================================
+// The adapter's term of dX under dropout:  dX += D c (sU At^T), in place, bf16.
+// A warp takes 16 tokens x 32 columns: the rank-r product on mma.m16n8k16 from
+// 16-byte words of both factors (a lane's words hold the same eight j), through
+// shared memory to eight consecutive columns a lane, one Philox block's mask.
+// Bytes: dX read and written; the generator costs about as much.
+// ===========================================================================
+__global__ void __launch_bounds__(256, 3)
+k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restrict__ At, int RP, int M, int K,
+              __nv_bfloat16* dX, const __grid_constant__ DropoutKeys keys) {
+  __shared__ __align__(16) float s_ad[8][16][36];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int m0 = (int)blockIdx.y * 128 + warp * 16, k0 = (int)blockIdx.x * 32;
+  if (m0 >= M) return;
+  float acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
+  for (int j = 8 * t; j < RP; j += 32) {
+    uint4 a[2], b[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      a[h] = m0 + 8 * h + g < M ? __ldg(reinterpret_cast<const uint4*>(sU + (int64_t)(m0 + 8 * h + g) * RP + j))
+                                : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)                    // K % 32 == 0
+      b[i] = __ldg(reinterpret_cast<const uint4*>(At + (int64_t)(k0 + 8 * i + g) * RP + j));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mma_16816(acc[i], a[0].x, a[1].x, a[0].y, a[1].y, b[i].x, b[i].y);
+      mma_16816(acc[i], a[0].z, a[1].z, a[0].w, a[1].w, b[i].z, b[i].w);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      *reinterpret_cast<float2*>(&s_ad[warp][g + 8 * h][8 * i + 2 * t]) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = 8 * q + (lane >> 2), col = 8 * (lane & 3);
+    if (m0 + row >= M) continue;
+    const int64_t e = (int64_t)(m0 + row) * K + k0 + col;
+    uint4 v = *reinterpret_cast<const uint4*>(dX + e);
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+    const Draw draw = draw8((uint64_t)e >> 3, keys);
+    const float* ad = &s_ad[warp][row][col];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = draw.keep(2 * i, keys.thr8) ? __fmaf_rn(ad[2 * i], keys.scale, bf16_lo(w[i])) : bf16_lo(w[i]);
+      const float b = draw.keep(2 * i + 1, keys.thr8) ? __fmaf_rn(ad[2 * i + 1], keys.scale, bf16_hi(w[i])) : bf16_hi(w[i]);
+      w[i] = pack_bf16x2(a, b);
+    }
+    *reinterpret_cast<uint4*>(dX + e) = v;
+  }
+}
+
+void launch_mx_rank_add(const void* sU, const void* At, int RP, int M, int K, void* dX, const Dropout& drop,
+                        cudaStream_t s) {
+  const dim3 grid((unsigned)(K / 32), (unsigned)((M + 127) / 128));
+  k_mx_rank_add<<<grid, 256, 0, s>>>((const __nv_bfloat16*)sU, (const __nv_bfloat16*)At, RP, M, K, (__nv_bfloat16*)dX,
+                                     make_keys(drop));
 }
 
 }  // namespace qnf4
