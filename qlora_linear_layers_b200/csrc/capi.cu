@@ -741,34 +741,42 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
   const bool nv = w->format == QLORA_NVFP4;
   float* xr = nv ? reinterpret_cast<float*>(wsb + lay.xr) : nullptr;
   const float scale = r ? alpha / (float)r : 0.0f;
-  // few tokens: quantisation and T in one launch, the adapter in the product's
-  // epilogue, the weight's read begun before either is done
-  const bool few = M <= kMxFewTokens && K <= kMxPrepMaxK && !dr.on;
+  // few tokens: quantisation and T in one launch, and the product as its
+  // dependent; otherwise quantisation, X' when dropped out, T, and where the
+  // adapter runs as K steps of the product the factor that reads B
+  const bool epi = mx_adapter_in_epilogue((int)M, (int)N, (int)K, d->sms);
+  const bool prep = epi && M <= kMxPrepTokens && K <= kMxPrepMaxK && !dr.on;
   MxAdapter ad;
   int n = 2;
-  if (few) {
-    launch_mx_prep(X, (int)M, (int)K, A, r, w->format, wsb + lay.xq, wsb + lay.xs, xr, scale, wsb + lay.sT, T_save,
-                   d->status, s);
-    ad.r = r; ad.sT = wsb + lay.sT; ad.B = B;
-  } else {
-    launch_mx_quantize(X, QLORA_BF16, M, K, K, w->format, wsb + lay.xq, wsb + lay.xs, xr, d->status, s);
-  }
-  if (r && !few) {
+  if (r && epi) {
+    ad.r = r;
+    ad.sT = wsb + lay.sT;
+    ad.B = B;
+  } else if (r) {
     ad.RP = padded_rank(r);
     ad.tok = wsb + lay.sT;
     ad.wt = B;
-    const void* Xd = X;
-    if (dr.on) {
-      launch_dropout(X, K, nullptr, 0, wsb + lay.xd, K, QLORA_BF16, M, K, 0, dr, s);
-      Xd = wsb + lay.xd;
-      ++n;
-    }
-    st = launch_mx_down(Xd, A, (int)M, (int)K, r, ad.RP, scale, xr, wsb + lay.sT, T_save, d->status, s, d->sms);
-    if (st) return st;
-    ++n;
     if (nv || r < ad.RP) {
       launch_mx_pad_rows(B, N, r, r, ad.RP, nv ? w->row_scale : nullptr, wsb + lay.Bpad, s);
       ad.wt = wsb + lay.Bpad;
+      ++n;
+    }
+  }
+  if (prep) {
+    launch_mx_prep(X, (int)M, (int)K, A, r, w->format, wsb + lay.xq, wsb + lay.xs, xr, scale, wsb + lay.sT, T_save,
+                   d->status, s);
+  } else {
+    launch_mx_quantize(X, QLORA_BF16, M, K, K, w->format, wsb + lay.xq, wsb + lay.xs, xr, d->status, s);
+    if (r) {
+      const void* Xd = X;
+      if (dr.on) {
+        launch_dropout(X, K, nullptr, 0, wsb + lay.xd, K, QLORA_BF16, M, K, 0, dr, s);
+        Xd = wsb + lay.xd;
+        ++n;
+      }
+      st = launch_mx_down(Xd, A, (int)M, (int)K, r, epi ? r : ad.RP, scale, epi ? nullptr : xr, wsb + lay.sT, T_save,
+                          !dr.on, d->status, s, d->sms);
+      if (st) return st;
       ++n;
     }
   }
@@ -781,7 +789,7 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
   cudaEvent_t e0, e1;
   take_gemm_events(&e0, &e1);
   if (e0) cudaEventRecord(e0, s);
-  st = launch_mx_gemm(&x, w, ad, few, Y, d->status, s, d->sms);
+  st = launch_mx_gemm(&x, w, ad, true, Y, d->status, s, d->sms);
   if (e1) cudaEventRecord(e1, s);
   if (st) return st;
   st = launch_status();
@@ -819,12 +827,13 @@ int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY,
       ++n;
     }
     if (!T) {
-      st = launch_mx_down(Xd, A, (int)M, (int)K, r, RP, scale, nullptr, nullptr, wsb + lay.T, d->status, s, d->sms);
+      st = launch_mx_down(Xd, A, (int)M, (int)K, r, RP, scale, nullptr, nullptr, wsb + lay.T, false, d->status, s,
+                          d->sms);
       if (st) return st;
       T = wsb + lay.T;
       ++n;
     }
-    st = launch_mx_down(dY, wsb + lay.Bt, (int)M, (int)N, r, RP, scale, nullptr, sU, nullptr, d->status, s, d->sms);
+    st = launch_mx_down(dY, wsb + lay.Bt, (int)M, (int)N, r, RP, scale, nullptr, sU, nullptr, false, d->status, s, d->sms);
     if (st) return st;
     n += 3;                                        // transpose, sU, outer
   }

@@ -30,10 +30,10 @@ struct Dropout;
 void launch_mx_rank_add(const void* sU, const void* At, int RP, int M, int K, void* dX, const Dropout& drop,
                         cudaStream_t s);
 
-// Few tokens (M <= kMxFewTokens): X [M, K] bf16 quantised (scales of rows past M
+// Few tokens (M <= kMxPrepTokens): X [M, K] bf16 quantised (scales of rows past M
 // are left as they are) and, with r > 0 and T = X A^T, sT [M, r] = RNbf16(s T)
 // and T_save = RNbf16(T) (may be null).  K <= kMxPrepMaxK.
-constexpr int kMxFewTokens = 32;
+constexpr int kMxPrepTokens = 64;
 constexpr int kMxPrepMaxK = 3 * 256 * 32;
 void launch_mx_prep(const void* X, int M, int K, const void* A, int r, int format, uint8_t* packed, uint8_t* scales,
                     float* row_scale, float s, void* sT, void* T_save, int* status, cudaStream_t st);
@@ -50,8 +50,8 @@ void launch_mx_pad_rows(const void* in, int64_t rows, int r, int ldi, int RP, co
 
 // The adapter term of a product: none (RP = r = 0), bf16 factors of RP columns
 // (a multiple of 64) as extra K steps, tok [M, RP] and wt [N, RP] (with NVFP4
-// divided by the row scales of x and w), or, for few tokens, sT [M, r] and B
-// [N, r] as they are, added by the epilogue.
+// divided by the row scales of x and w), or, where mx_adapter_in_epilogue, sT
+// [M, r] and B [N, r] as they are, added by the epilogue.
 struct MxAdapter {
   int RP = 0;
   const void* tok = nullptr;
@@ -61,17 +61,25 @@ struct MxAdapter {
   const void* B = nullptr;
 };
 
+// Whether the product of these sizes adds the adapter in its epilogue: with few
+// tokens, and where the paired kernel has one round of tiles (a longer one
+// would wait for its epilogues; one round saves the launch that prepares B).
+bool mx_adapter_in_epilogue(int M, int N, int K, int num_sms);
+
 // Y[M, N] = deq(x) deq(w)^T + the adapter's term.  after_prep: launched as the
-// dependent of launch_mx_prep, which wrote x and sT.  Returns QLORA_OK or
-// QLORA_ERR_CUDA.
+// dependent of the kernel before it (launch_mx_prep, launch_mx_quantize or
+// launch_mx_down), which is the last that writes x, sT or tok; w and its adapter
+// factor were complete before that one began.  QLORA_OK or QLORA_ERR_CUDA.
 int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
                    int* status, cudaStream_t s, int num_sms);
 
 // With S = Z R^T, Z [M, L], R [r, L] bf16: pad [M, RP] = RNbf16(s S /
 // row_scale[m]), zero beyond r (row_scale null: no division), and out [M, r] =
-// RNbf16(S); either may be null.  L % 8 == 0.  QLORA_OK or QLORA_ERR_CUDA.
+// RNbf16(S); either may be null.  L % 8 == 0.  dependent: launched beside the
+// kernel before it (launch_mx_quantize), which wrote row_scale and nothing else
+// that is read here.  QLORA_OK or QLORA_ERR_CUDA.
 int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, float s, const float* row_scale,
-                   void* pad, void* out, int* status, cudaStream_t st, int num_sms);
+                   void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms);
 
 // dA [r, K] = RNbf16(sU^T Xd), dB [N, r] = RNbf16(s dY^T T) over M tokens; sU has
 // ldu columns.  QLORA_OK or QLORA_ERR_CUDA.

@@ -23,9 +23,10 @@
 //    groups) and issues four K = 64 MMAs;
 //  * warps 2-5: epilogue, tensor memory -> cluster reduction -> bf16.
 //
-// The adapter s (X A^T) B^T runs first, in rank 0, as RP / 64 bf16 K steps
-// (kind::f16) into the same accumulator; its MMAs complete before the first
-// block-scaled one is issued, since the two kinds need not run in order.
+// The adapter's term s (X A^T) B^T comes from the epilogue warps, on warp-level
+// MMAs while the others run (up to 32 tokens), or runs first, in rank 0, as RP /
+// 64 bf16 K steps (kind::f16) into the same accumulator; these complete before the
+// first block-scaled MMA is issued, since the two kinds need not run in order.
 // Every wait is bounded (QLORA_ERR_TIMEOUT).
 
 #include <algorithm>
@@ -77,11 +78,6 @@ struct Smem {
 template <int FMT, int BN>
 constexpr size_t smem_bytes() { return sizeof(Smem<FMT, BN>) + 1024; }
 
-// Wait for the grid that this one was launched after (returns at once when the
-// launch had no such attribute).
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 __device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
@@ -175,7 +171,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   const int n0 = (int)(blockIdx.x >> log_splits) * BW, m0 = blockIdx.y * BN;
   const int nk_all = (p.K + 255) / 256;
   const int k0 = (int)(((int64_t)nk_all * rank) >> log_splits), k1 = (int)(((int64_t)nk_all * (rank + 1)) >> log_splits);
-  const int na = rank == 0 ? p.na : 0;
+  const int na = !Sh::OWN_PART && rank == 0 ? p.na : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
@@ -445,6 +441,14 @@ static int launch_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const 
 
 }  // namespace mx
 
+bool mx_adapter_in_epilogue(int M, int N, int K, int num_sms) {
+  mx::Args a{};
+  a.M = M; a.N = N; a.K = K;
+  int ls = 0;
+  return M <= mx::kFewTokens ||
+         (mx::pair_rounds(a, num_sms) == 1 && mx::pair_cost(a, num_sms) <= mx::split_cost(a, 128, num_sms, &ls));
+}
+
 int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
                    int* status, cudaStream_t s, int num_sms) {
   mx::Args a{};
@@ -461,8 +465,8 @@ int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxA
   // 9.2 us against 10.6), a split contraction where a long one meets few weight
   // rows (W 1024 x 18944, 128 tokens: 12.7 us against 23.1).
   int ls = 0;
-  if (a.M > kMxFewTokens && mx::pair_cost(a, num_sms) <= mx::split_cost(a, 128, num_sms, &ls))
-    return mx::launch_gemm_pair(x, w, ad, a, s, num_sms);
+  if (a.M > mx::kFewTokens && mx::pair_cost(a, num_sms) <= mx::split_cost(a, 128, num_sms, &ls))
+    return mx::launch_gemm_pair(x, w, ad, after_prep, a, s, num_sms);
   return x->format == QLORA_NVFP4 ? mx::launch_fmt<QLORA_NVFP4>(x, w, ad, after_prep, a, s, num_sms)
                                   : mx::launch_fmt<QLORA_MXFP4>(x, w, ad, after_prep, a, s, num_sms);
 }

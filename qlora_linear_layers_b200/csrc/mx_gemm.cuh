@@ -22,7 +22,7 @@ struct Args {
   __nv_bfloat16* out;
   int M, N, K;
   int na;                   // adapter K steps
-  int r;                    // rank of the adapter added by the epilogue (few tokens), 0: none
+  int r;                    // rank of the adapter added by the epilogue, 0: none
   const __nv_bfloat16* sT;  // [M, r]
   const __nv_bfloat16* B;   // [N, r]
   int* status;
@@ -30,8 +30,17 @@ struct Args {
 
 // mx_gemm_pair.cu
 int64_t pair_cost(const Args& a, int num_sms);
-int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
-                     cudaStream_t s, int num_sms);
+int pair_rounds(const Args& a, int num_sms);
+int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep,
+                     const Args& a, cudaStream_t s, int num_sms);
+
+constexpr int kFewTokens = 32;                     // up to here the kernel for few tokens
+
+// Wait for the grid that this one was launched after (returns at once when the
+// launch had no such attribute).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // True in one lane of a converged warp.  The tensor-core and TMA instructions
 // take their operands from uniform registers; behind an elect.sync the compiler

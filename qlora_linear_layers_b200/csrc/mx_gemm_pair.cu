@@ -25,6 +25,8 @@
 //    192 tokens, whose MMAs do 8 % less per cycle.
 // The adapter's bf16 K steps (kind::f16) come first and are complete before the
 // block-scaled MMAs of the tile begin: MMAs of two kinds need not run in order.
+// With one round of tiles the epilogue adds the adapter instead, on warp-level
+// MMAs whose accumulator fragments are the ones it holds.
 //
 // Every scale tile comes with the stage: each CTA loads the scales of its own
 // 128 weight rows and of all PN tokens (one or two 128-row blocks), and the
@@ -41,6 +43,7 @@
 #include "gemm.h"
 #include "mx.h"
 #include "mx_gemm.cuh"
+#include "mx_mma.cuh"
 
 namespace qnf4 {
 namespace mx {
@@ -108,7 +111,8 @@ struct PairSmem {
   int abort;
 };
 
-template <int FMT, int PN>
+// ADD: the epilogue adds the adapter (p.r > 0).
+template <int FMT, int PN, bool ADD>
 __global__ void __launch_bounds__(P_THREADS, 1)
 k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                const __grid_constant__ CUtensorMap tm_sw, const __grid_constant__ CUtensorMap tm_sx,
@@ -161,6 +165,7 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
+      grid_dependency_wait();
       for (int tile = cluster; tile < n_tiles && ok; tile += n_clusters) {
         const int n0 = (tile % tiles_n) * (2 * BW) + (int)rank * BW;
         const int mt = (tile / tiles_n) * PN, m0 = mt + (int)rank * PNH;
@@ -251,6 +256,8 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     // this lane's row of the four blocks of a stmatrix: token lane % 8, outputs 8 (lane / 8) ..
     const uint32_t row_off = (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
     uint32_t tp = 0;
+    bool ok = true;
+    grid_dependency_wait();
     for (int tile = cluster; tile < n_tiles; tile += n_clusters, tp ^= 1) {
       const int nw = (tile % tiles_n) * (2 * BW) + (int)rank * BW + quad * 32;     // the warp's outputs
       const int mt = (tile / tiles_n) * PN, m0 = mt + half * HC;
@@ -263,14 +270,16 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
         for (int i = threadIdx.x - 64; i < PN; i += 32 * P_EPI) S.rx[tp][i] = mt + i < p.M ? p.xr[mt + i] : 0.0f;
         asm volatile("bar.sync 1, %0;" :: "n"(32 * P_EPI) : "memory");
       }
-      if (!mbar_wait_cluster(&S.acc_full, tp, abort, p.status)) break;
+      // after a wait that gave up the tiles pass without results, so that every
+      // warp comes to every barrier
+      if (!(ok = ok && mbar_wait_cluster(&S.acc_full, tp, abort, p.status))) continue;
       __syncwarp();
       tc_fence_after();
-      uint32_t v[HC / 32][2][16];
+      float v[HC / 32][2][4][4];                   // [chunk][16 outputs][8 tokens][fragment]
 #pragma unroll
       for (int c = 0; c < HC / 32; ++c)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) tmem_ld_16x32(taddr + 32 * c + ((uint32_t)(16 * h) << 16), v[c][h]);
+        for (int h = 0; h < 2; ++h) tmem_ld_16x32(taddr + 32 * c + ((uint32_t)(16 * h) << 16), reinterpret_cast<uint32_t*>(v[c][h]));
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
@@ -279,6 +288,40 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       for (int c = 0; c < HC / 32; ++c) {
         const int m = m0 + 32 * c;
         if (m >= p.M || nw >= p.N) break;
+        if (NV) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 rx = *reinterpret_cast<const float2*>(&S.rx[tp][half * HC + 32 * c + 8 * j + 2 * (lane & 3)]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {          // outputs 8 i + g
+              float* f = &v[c][i >> 1][j][2 * (i & 1)];
+              f[0] = __fmul_rn(f[0], __fmul_rn(rx.x, rw[i]));
+              f[1] = __fmul_rn(f[1], __fmul_rn(rx.y, rw[i]));
+            }
+          }
+        }
+        if constexpr (ADD) {
+          // += B sT^T; a lane's words of both hold the same eight k
+          for (int k = 8 * (lane & 3); k - 8 * (lane & 3) < p.r; k += 32) {
+            uint4 b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              b[i] = k < p.r && nw + 8 * i + g < p.N
+                         ? __ldg(reinterpret_cast<const uint4*>(p.B + (int64_t)(nw + 8 * i + g) * p.r + k))
+                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint4 t = k < p.r && m + 8 * j + g < p.M
+                                  ? *reinterpret_cast<const uint4*>(p.sT + (int64_t)(m + 8 * j + g) * p.r + k)
+                                  : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                mma_16816(v[c][h][j], b[2 * h].x, b[2 * h + 1].x, b[2 * h].y, b[2 * h + 1].y, t.x, t.y);
+                mma_16816(v[c][h][j], b[2 * h].z, b[2 * h + 1].z, b[2 * h].w, b[2 * h + 1].w, t.z, t.w);
+              }
+            }
+          }
+        }
         uint8_t* out = S.out[e][c & 1];
         if (lane == 0) store_wait_read<1>();       // the store before the last one has left its chunk
         __syncwarp();
@@ -286,18 +329,8 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
 #pragma unroll
         for (int j = 0; j < 4; ++j) {              // tokens 8 j .. 8 j + 7
           uint32_t o[4];                           // outputs 8 i .. 8 i + 7
-          float2 rx = make_float2(1.0f, 1.0f);
-          if (NV) rx = *reinterpret_cast<const float2*>(&S.rx[tp][half * HC + 32 * c + 8 * j + 2 * (lane & 3)]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float a = __uint_as_float(v[c][i >> 1][4 * j + 2 * (i & 1)]);
-            float b = __uint_as_float(v[c][i >> 1][4 * j + 2 * (i & 1) + 1]);
-            if (NV) {
-              a = __fmul_rn(a, __fmul_rn(rx.x, rw[i]));
-              b = __fmul_rn(b, __fmul_rn(rx.y, rw[i]));
-            }
-            o[i] = pack_bf16x2(a, b);
-          }
+          for (int i = 0; i < 4; ++i) o[i] = pack_bf16x2(v[c][i >> 1][j][2 * (i & 1)], v[c][i >> 1][j][2 * (i & 1) + 1]);
           stmatrix_x4_t(to + 512 * j, o[0], o[1], o[2], o[3]);
         }
         if (whole) {
@@ -358,9 +391,17 @@ int64_t pair_cost(const Args& a, int num_sms) {
   return 520 + cycles * 10 / 196;
 }
 
-template <int FMT, int PN>
-static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
-                       cudaStream_t s, int num_sms) {
+int pair_rounds(const Args& a, int num_sms) {
+  int64_t cycles;
+  const int pn = pair_tokens(a, num_sms, &cycles);
+  const int64_t tiles = (int64_t)((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + pn - 1) / pn);
+  const int pairs = std::max(1, num_sms / 2);
+  return (int)((tiles + pairs - 1) / pairs);
+}
+
+template <int FMT, int PN, bool ADD>
+static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep,
+                       const Args& a, cudaStream_t s, int num_sms) {
   using Sh = PairShape<FMT, PN>;
   CUtensorMap tw, tx, tsw, tsx, twa, txa, to;
   const uint64_t kb = (uint64_t)a.K / 2;
@@ -379,39 +420,44 @@ static int launch_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const
   constexpr size_t bytes = sizeof(PairSmem<FMT, PN>) + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<unsigned long long> attr_devs{0};
-  set_smem_attr_once(k_mx_gemm_pair<FMT, PN>, (int)bytes, attr_devs);
+  set_smem_attr_once(k_mx_gemm_pair<FMT, PN, ADD>, (int)bytes, attr_devs);
   const int tiles = ((a.N + 2 * BW - 1) / (2 * BW)) * ((a.M + PN - 1) / PN);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * std::max(1, std::min(tiles, num_sms / 2)), 1, 1);
   cfg.blockDim = dim3(P_THREADS, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_mx_gemm_pair<FMT, PN>, tw, tx, tsw, tsx, twa, txa, to, a) == cudaSuccess
+  cfg.numAttrs = after_prep ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_mx_gemm_pair<FMT, PN, ADD>, tw, tx, tsw, tsx, twa, txa, to, a) == cudaSuccess
              ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 template <int FMT>
-static int launch_pair_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
-                           cudaStream_t s, int num_sms) {
+static int launch_pair_fmt(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep,
+                           const Args& a, cudaStream_t s, int num_sms) {
   int64_t cycles;
-  switch (pair_tokens(a, num_sms, &cycles)) {
-    case 128: return launch_pair<FMT, 128>(x, w, ad, a, s, num_sms);
-    case 192: return launch_pair<FMT, 192>(x, w, ad, a, s, num_sms);
-    default: return launch_pair<FMT, 256>(x, w, ad, a, s, num_sms);
-  }
+  const int pn = pair_tokens(a, num_sms, &cycles);
+  if (a.r)
+    return pn == 128   ? launch_pair<FMT, 128, true>(x, w, ad, after_prep, a, s, num_sms)
+           : pn == 192 ? launch_pair<FMT, 192, true>(x, w, ad, after_prep, a, s, num_sms)
+                       : launch_pair<FMT, 256, true>(x, w, ad, after_prep, a, s, num_sms);
+  return pn == 128   ? launch_pair<FMT, 128, false>(x, w, ad, after_prep, a, s, num_sms)
+         : pn == 192 ? launch_pair<FMT, 192, false>(x, w, ad, after_prep, a, s, num_sms)
+                     : launch_pair<FMT, 256, false>(x, w, ad, after_prep, a, s, num_sms);
 }
 
-int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, const Args& a,
-                     cudaStream_t s, int num_sms) {
-  return x->format == QLORA_NVFP4 ? launch_pair_fmt<QLORA_NVFP4>(x, w, ad, a, s, num_sms)
-                                  : launch_pair_fmt<QLORA_MXFP4>(x, w, ad, a, s, num_sms);
+int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep,
+                     const Args& a, cudaStream_t s, int num_sms) {
+  return x->format == QLORA_NVFP4 ? launch_pair_fmt<QLORA_NVFP4>(x, w, ad, after_prep, a, s, num_sms)
+                                  : launch_pair_fmt<QLORA_MXFP4>(x, w, ad, after_prep, a, s, num_sms);
 }
 
 }  // namespace mx

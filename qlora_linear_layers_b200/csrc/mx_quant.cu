@@ -280,6 +280,7 @@ __global__ void __launch_bounds__(512)
 k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __restrict__ packed,
               uint8_t* __restrict__ scales, float* __restrict__ row_scale, int* status) {
   __shared__ uint32_t s_max[16];
+  grid_launch_dependents();
   const int64_t row = blockIdx.x;                  // rows past the last write the padding's zero scales
   quantise_row<T, FMT, KEEP>(X + row * ld, row < rows, row, K, threadIdx.x, blockDim.x, packed, scales, row_scale,
                              status, s_max);
@@ -334,7 +335,7 @@ k_mx_prep(const __nv_bfloat16* __restrict__ X, int M, int K, const __nv_bfloat16
   __shared__ uint32_t s_max[16];
   __shared__ float s_warp[8][MT * 8];              // [warp][token * 8 + row of A]
   __shared__ float s_rank[8][MT * 8];              // rank 0: the ranks' sums
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if ((int)blockIdx.x >= r) {
     const int row = (int)blockIdx.x - r;
@@ -401,10 +402,12 @@ void launch_mx_prep(const void* X, int M, int K, const void* A, int r, int forma
   };
   if (format == QLORA_NVFP4) {
     if (M <= 16) run(k_mx_prep<QLORA_NVFP4, 16>);
-    else run(k_mx_prep<QLORA_NVFP4, 32>);
+    else if (M <= 32) run(k_mx_prep<QLORA_NVFP4, 32>);
+    else run(k_mx_prep<QLORA_NVFP4, 64>);
   } else {
     if (M <= 16) run(k_mx_prep<QLORA_MXFP4, 16>);
-    else run(k_mx_prep<QLORA_MXFP4, 32>);
+    else if (M <= 32) run(k_mx_prep<QLORA_MXFP4, 32>);
+    else run(k_mx_prep<QLORA_MXFP4, 64>);
   }
 }
 

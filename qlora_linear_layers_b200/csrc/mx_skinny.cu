@@ -102,7 +102,7 @@ __device__ __forceinline__ void store2(const Args& g, const Problem& p, const fl
       a = __fdiv_rn(a, d);
       b = __fdiv_rn(b, d);
     }
-    if (p.pad) *reinterpret_cast<uint32_t*>(p.pad + (int64_t)row * g.RP + col) = pack_bf16x2(a, b);
+    if (p.pad && col < g.RP) *reinterpret_cast<uint32_t*>(p.pad + (int64_t)row * g.RP + col) = pack_bf16x2(a, b);
     if (p.out && col < g.r) *reinterpret_cast<uint32_t*>(p.out + (int64_t)row * g.r + col) = pack_bf16x2(v[0], v[1]);
   }
 }
@@ -132,7 +132,7 @@ __device__ __forceinline__ void store8(const Args& g, const Problem& p, const fl
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], d);
   }
-  if (p.pad) *reinterpret_cast<uint4*>(p.pad + (int64_t)row * g.RP + col) = pack8(f);
+  if (p.pad && col < g.RP) *reinterpret_cast<uint4*>(p.pad + (int64_t)row * g.RP + col) = pack8(f);
   if (p.out && col < g.r) *reinterpret_cast<uint4*>(p.out + (int64_t)row * g.r + col) = pack8(v);
 }
 
@@ -142,6 +142,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
             const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
             const __grid_constant__ Args g) {
   extern __shared__ uint8_t smem_raw[];
+  grid_launch_dependents();
   Head& S = *smem_align1024<Head>(smem_raw);
   uint8_t* stages = reinterpret_cast<uint8_t*>(&S) + 1024;
   const int NS = g.ns, stage_bytes = A_BYTES + g.b_bytes;
@@ -228,6 +229,9 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     }
   } else {
     mbar_wait(&S.acc_full, 0, abort, g.status);
+    // as a dependent of the quantisation (whose row scales may be read below) this
+    // grid does not end before that one
+    mx::grid_dependency_wait();
   }
   __syncwarp();
   const int quad = warp & 3;
@@ -315,7 +319,7 @@ static void shape(Args& g, int num_sms) {
 
 template <bool OUTER>
 static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
-                  const Args& g, cudaStream_t s) {
+                  const Args& g, bool dependent, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_devs{0};
   set_smem_attr_once(k_mx_skinny<OUTER>, 224 * 1024, attr_devs);
   cudaLaunchConfig_t cfg = {};
@@ -323,20 +327,22 @@ static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMa
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = 2048 + (size_t)g.ns * (A_BYTES + g.b_bytes);
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1u << g.log_splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = dependent ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_mx_skinny<OUTER>, a0, b0, a1, b1, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 }  // namespace skinny
 
 int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, float s, const float* row_scale,
-                   void* pad, void* out, int* status, cudaStream_t st, int num_sms) {
+                   void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms) {
   using namespace skinny;
   Args g{};
   g.L = L;
@@ -349,7 +355,7 @@ int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, fl
   shape(g, num_sms);
   CUtensorMap a, b;
   if (!make_tmap_2d_bf16(&a, Z, L, M, L, 64, 128) || !make_tmap_2d_bf16(&b, R, L, r, L, 64, g.N)) return QLORA_ERR_CUDA;
-  return launch<false>(a, b, a, b, g, st);
+  return launch<false>(a, b, a, b, g, dependent, st);
 }
 
 int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, const void* dY, int N, const void* T,
@@ -368,7 +374,7 @@ int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, co
   if (!make_tmap_2d_bf16(&a0, Xd, K, M, K, 64, 64) || !make_tmap_2d_bf16(&b0, sU, r, M, ldu, 64, 64) ||
       !make_tmap_2d_bf16(&a1, dY, N, M, N, 64, 64) || !make_tmap_2d_bf16(&b1, T, r, M, r, 64, 64))
     return QLORA_ERR_CUDA;
-  return launch<true>(a0, b0, a1, b1, g, st);
+  return launch<true>(a0, b0, a1, b1, g, false, st);
 }
 
 // ===========================================================================
