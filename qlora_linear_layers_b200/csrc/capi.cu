@@ -134,11 +134,11 @@ MxFwdWs mx_fwd_ws(int64_t M, int64_t N, int64_t K, int r, bool dropout) {
   return w;
 }
 
-// Its backward: Wt = deq(W)^T [K, N], and with an adapter T [M, r] (recomputed
-// when not passed), sU [M, RP], At [K, RP], Bt [r, N] and, with dropout, X'
-// [M, K] (all bf16).
+// Its backward: Wt = deq(W)^T [K, N] where dX does not expand the weight inside,
+// and with an adapter T [M, r] (recomputed when not passed), sU [M, RP], At [K, RP]
+// and, with dropout, X' [M, K] (all bf16).
 struct MxBwdWs {
-  size_t Wt, T, sU, At, Bt, xd, total;
+  size_t Wt, T, sU, At, xd, total;
 };
 MxBwdWs mx_bwd_ws(int64_t M, int64_t N, int64_t K, int r, bool dropout) {
   MxBwdWs w{};
@@ -149,7 +149,6 @@ MxBwdWs mx_bwd_ws(int64_t M, int64_t N, int64_t K, int r, bool dropout) {
     w.T = off;  off += align256((size_t)M * r * 2);
     w.sU = off; off += align256((size_t)M * RP * 2);
     w.At = off; off += align256((size_t)K * RP * 2);
-    w.Bt = off; off += align256((size_t)r * N * 2);
     if (dropout) { w.xd = off; off += align256((size_t)M * K * 2); }
   }
   w.total = off;
@@ -774,7 +773,7 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
         Xd = wsb + lay.xd;
         ++n;
       }
-      st = launch_mx_down(Xd, A, (int)M, (int)K, r, epi ? r : ad.RP, scale, epi ? nullptr : xr, wsb + lay.sT, T_save,
+      st = launch_mx_down(Xd, A, false, (int)M, (int)K, r, epi ? r : ad.RP, scale, epi ? nullptr : xr, wsb + lay.sT, T_save,
                           !dr.on, d->status, s, d->sms);
       if (st) return st;
       ++n;
@@ -818,44 +817,54 @@ int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY,
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   void *Wt = wsb + lay.Wt, *sU = wsb + lay.sU, *At = wsb + lay.At;
   const void* Xd = X;
-  int n = 2;                                       // dequant_t and the GEMM
+  const int na = r && !dr.on ? RP / 64 : 0;         // with dropout the adapter's term needs the keep mask
+  const bool inside = mx_dx_expands_inside((int)M, (int)N, (int)K, na, d->sms);
+  int n = 1;
   if (r) {
-    launch_mx_transpose(A, B, r, (int)K, (int)N, RP, At, wsb + lay.Bt, s);
+    if (!inside || dr.on) {
+      launch_mx_transpose(A, r, (int)K, RP, At, s);
+      ++n;
+    }
     if (dr.on) {
       launch_dropout(X, K, nullptr, 0, wsb + lay.xd, K, QLORA_BF16, M, K, 0, dr, s);
       Xd = wsb + lay.xd;
       ++n;
     }
     if (!T) {
-      st = launch_mx_down(Xd, A, (int)M, (int)K, r, RP, scale, nullptr, nullptr, wsb + lay.T, false, d->status, s,
+      st = launch_mx_down(Xd, A, false, (int)M, (int)K, r, RP, scale, nullptr, nullptr, wsb + lay.T, false, d->status, s,
                           d->sms);
       if (st) return st;
       T = wsb + lay.T;
       ++n;
     }
-    st = launch_mx_down(dY, wsb + lay.Bt, (int)M, (int)N, r, RP, scale, nullptr, sU, nullptr, false, d->status, s, d->sms);
+    st = launch_mx_down(dY, B, true, (int)M, (int)N, r, RP, scale, nullptr, sU, nullptr, false, d->status, s, d->sms);
     if (st) return st;
-    n += 3;                                        // transpose, sU, outer
+    n += 2;                                        // sU, outer
   }
-  launch_mx_dequant_t(w, Wt, s);
-  // dX[M, K] = dY Wt^T + sU At^T; with dropout the adapter's term needs the keep
-  // mask: the GEMM writes dY W' alone and a rank-r pass adds D * c * (s U A)
-  GemmArgs a{};
-  a.out = static_cast<__nv_bfloat16*>(dX);
-  a.wad = static_cast<const __nv_bfloat16*>(At);
-  a.RP = RP;
-  a.Mtok = (int)M; a.Nout = (int)K; a.Kc = (int)N;
-  a.na = r && !dr.on ? RP / 64 : 0;
-  a.status = d->status;
-  const void *tokad = r ? sU : dY, *wad = r ? At : Wt;    // unread (na = 0) without an adapter
   cudaEvent_t e0, e1;
   take_gemm_events(&e0, &e1);
-  if (e0) cudaEventRecord(e0, s);
-  st = K > 128 ? launch_qlora_gemm_pair(a, dY, tokad, wad, Wt, RP, s, d->sms)
-               : launch_qlora_gemm(MODE_BF16, a, dY, tokad, wad, Wt, RP, s, d->sms);
+  if (inside) {
+    if (e0) cudaEventRecord(e0, s);
+    st = launch_mx_dx(w, dY, (int)M, A, r, sU, RP, na, dX, d->status, s, d->sms);
+  } else {
+    launch_mx_dequant_t(w, Wt, s);
+    ++n;
+    // dX[M, K] = dY Wt^T + sU At^T
+    GemmArgs a{};
+    a.out = static_cast<__nv_bfloat16*>(dX);
+    a.wad = static_cast<const __nv_bfloat16*>(At);
+    a.RP = RP;
+    a.Mtok = (int)M; a.Nout = (int)K; a.Kc = (int)N;
+    a.na = na;
+    a.status = d->status;
+    const void *tokad = r ? sU : dY, *wad = r ? At : Wt;  // unread (na = 0) without an adapter
+    if (e0) cudaEventRecord(e0, s);
+    st = K > 128 ? launch_qlora_gemm_pair(a, dY, tokad, wad, Wt, RP, s, d->sms)
+                 : launch_qlora_gemm(MODE_BF16, a, dY, tokad, wad, Wt, RP, s, d->sms);
+  }
   if (e1) cudaEventRecord(e1, s);
   if (st) return st;
-  if (dr.on) {
+  if (dr.on) {                                     // dX += D * c * (s U A)
     launch_mx_rank_add(sU, At, RP, (int)M, (int)K, dX, dr, s);
     ++n;
   }

@@ -73,21 +73,27 @@ bool mx_adapter_in_epilogue(int M, int N, int K, int num_sms);
 int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
                    int* status, cudaStream_t s, int num_sms);
 
-// With S = Z R^T, Z [M, L], R [r, L] bf16: pad [M, RP] = RNbf16(s S /
+// With S = Z R^T, Z [M, L] and R [r, L] (r_rows: R^T [L, r]) bf16: pad [M, RP] = RNbf16(s S /
 // row_scale[m]), zero beyond r (row_scale null: no division), and out [M, r] =
 // RNbf16(S); either may be null.  L % 8 == 0.  dependent: launched beside the
 // kernel before it (launch_mx_quantize), which wrote row_scale and nothing else
 // that is read here.  QLORA_OK or QLORA_ERR_CUDA.
-int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, float s, const float* row_scale,
-                   void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms);
+int launch_mx_down(const void* Z, const void* R, bool r_rows, int M, int L, int r, int RP, float s,
+                   const float* row_scale, void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms);
 
 // dA [r, K] = RNbf16(sU^T Xd), dB [N, r] = RNbf16(s dY^T T) over M tokens; sU has
 // ldu columns.  QLORA_OK or QLORA_ERR_CUDA.
 int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, const void* dY, int N, const void* T,
                     float s, void* dB, int M, int r, int* status, cudaStream_t st, int num_sms);
 
-// At [K, RP] = A [r, K]^T, zero beyond r, and Bt [r, N] = B [N, r]^T.
-void launch_mx_transpose(const void* A, const void* B, int r, int K, int N, int RP, void* At, void* Bt,
-                         cudaStream_t s);
+// At [K, RP] = A [r, K]^T, zero beyond r.
+void launch_mx_transpose(const void* A, int r, int K, int RP, void* At, cudaStream_t s);
+
+// dX [M, K] = dY deq(W) + sU A over RP = 64 na columns of sU [M, RP] (na = 0: the
+// first term alone), W expanded inside the product; mx_dx_expands_inside: whether
+// that is the faster way for these sizes.  QLORA_OK or QLORA_ERR_CUDA.
+bool mx_dx_expands_inside(int M, int N, int K, int na, int num_sms);
+int launch_mx_dx(const qlora_mx_tensor* w, const void* dY, int M, const void* A, int r, const void* sU, int RP, int na,
+                 void* dX, int* status, cudaStream_t s, int num_sms);
 
 }  // namespace qnf4

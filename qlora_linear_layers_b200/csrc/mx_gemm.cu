@@ -127,28 +127,6 @@ __device__ __forceinline__ void adapter_term(const __nv_bfloat16* B, int rows, c
   __syncwarp();
 }
 
-// Add the ranks' partial sums of NC token columns (in rank order), scale, store.
-template <int NC, bool NV>
-__device__ __forceinline__ void add_ranks(const Args& p, const float* part, int rank_stride, int splits, int m, int n,
-                                          float rw, const float* add, int add_pitch, bool odd, bool pairs) {
-  float sum[NC], rx[NC];
-#pragma unroll
-  for (int j = 0; j < NC; ++j) rx[j] = NV && m + j < p.M ? p.xr[m + j] : 0.0f;
-#pragma unroll
-  for (int j = 0; j < NC; ++j) sum[j] = part[j * 128];
-  for (int z = 1; z < splits; ++z)
-#pragma unroll
-    for (int j = 0; j < NC; ++j) sum[j] = __fadd_rn(sum[j], part[z * rank_stride + j * 128]);
-  uint32_t v[NC];
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    if (NV) sum[j] = __fmul_rn(sum[j], __fmul_rn(rx[j], rw));
-    if (add) sum[j] = __fadd_rn(sum[j], add[j * add_pitch]);
-    v[j] = __float_as_uint(sum[j]);
-  }
-  store_columns<NC>(p, v, m, n, n - (odd ? 1 : 0), odd, pairs);
-}
-
 template <int FMT, int BN>
 __global__ void __launch_bounds__(NUM_THREADS, 2)
 k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes

@@ -68,6 +68,19 @@ inline bool make_scale_tmap(CUtensorMap* tm, const uint8_t* scales, int format, 
   return make_tmap_3d(tm, scales, true, dims, strides, box, false);
 }
 
+// MN-major operand with a 128-byte swizzle: 64 consecutive elements of a row are
+// 128 bytes, eight rows 1024 bytes (the stride between groups of the
+// contraction), the next 64 elements `group` bytes away.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t group) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)(group >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;
+  d |= (uint64_t)2u << 61;
+  return d;
+}
+
 // 512-byte scale tile in shared memory: 32 rows of 16 bytes, no swizzle,
 // groups of eight rows 128 bytes apart.
 __device__ __forceinline__ uint64_t scale_desc(uint32_t addr) {
@@ -140,6 +153,39 @@ __device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const void* tma
       : "memory");
 }
 
+constexpr int kChunk = 32;                         // tokens of an output chunk
+
+// Warp-wide: 16 lanes x 32 columns of tensor memory; of every 8 columns thread t
+// gets columns 2 (t % 4), + 1 of lane t / 4 (v[4 j], v[4 j + 1]) and of lane
+// t / 4 + 8 (v[4 j + 2], v[4 j + 3]).
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 bf16 blocks of a warp, transposed: row i of block j goes to the
+// address that lane 8 j + i holds.
+__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+               :: "r"(addr), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t c0, int32_t c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
+               :: "l"(tmap), "r"(smem_u32(smem_src)), "r"(c0), "r"(c1) : "memory");
+}
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
+}
+
+
 // Store into another CTA of the cluster (address from mapa_shared).
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
@@ -176,6 +222,28 @@ __device__ __forceinline__ void store_columns(const Args& p, const uint32_t* v, 
     for (int j = 0; j < NC; ++j)
       if (m + j < p.M && n < p.N) p.out[(int64_t)(m + j) * p.N + n] = __float2bfloat16_rn(__uint_as_float(v[j]));
   }
+}
+
+// Add the ranks' partial sums of NC token columns (in rank order), scale, store.
+template <int NC, bool NV>
+__device__ __forceinline__ void add_ranks(const Args& p, const float* part, int rank_stride, int splits, int m, int n,
+                                          float rw, const float* add, int add_pitch, bool odd, bool pairs) {
+  float sum[NC], rx[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) rx[j] = NV && m + j < p.M ? p.xr[m + j] : 0.0f;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) sum[j] = part[j * 128];
+  for (int z = 1; z < splits; ++z)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) sum[j] = __fadd_rn(sum[j], part[z * rank_stride + j * 128]);
+  uint32_t v[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    if (NV) sum[j] = __fmul_rn(sum[j], __fmul_rn(rx[j], rw));
+    if (add) sum[j] = __fadd_rn(sum[j], add[j * add_pitch]);
+    v[j] = __float_as_uint(sum[j]);
+  }
+  store_columns<NC>(p, v, m, n, n - (odd ? 1 : 0), odd, pairs);
 }
 
 }  // namespace mx

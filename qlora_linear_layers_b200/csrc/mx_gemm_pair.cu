@@ -51,39 +51,6 @@ namespace mx {
 constexpr int P_EPI = 8;                           // epilogue warps
 constexpr int P_THREADS = 64 + 32 * P_EPI;         // warp 0 TMA, 1 MMA, 2-9 epilogue
 constexpr uint16_t kBoth = 0x3;
-constexpr int kChunk = 32;                         // tokens of an output chunk
-
-// Warp-wide: 16 lanes x 32 columns of tensor memory; of every 8 columns thread t
-// gets columns 2 (t % 4), + 1 of lane t / 4 (v[4 j], v[4 j + 1]) and of lane
-// t / 4 + 8 (v[4 j + 2], v[4 j + 3]).
-__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, uint32_t* v) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Four 8 x 8 bf16 blocks of a warp, transposed: row i of block j goes to the
-// address that lane 8 j + i holds.
-__device__ __forceinline__ void stmatrix_x4_t(uint32_t addr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
-  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
-               :: "r"(addr), "r"(r0), "r"(r1), "r"(r2), "r"(r3) : "memory");
-}
-
-__device__ __forceinline__ void tma_store_2d(const void* tmap, const void* smem_src, int32_t c0, int32_t c1) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];"
-               :: "l"(tmap), "r"(smem_u32(smem_src)), "r"(c0), "r"(c1) : "memory");
-}
-__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void store_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(N) : "memory");
-}
-
-
 template <int FMT, int PN>
 struct PairShape {
   static_assert(PN % 64 == 0 && PN <= 256, "token tile");

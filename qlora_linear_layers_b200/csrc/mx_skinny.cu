@@ -1,12 +1,12 @@
 // The adapter's products of the microscaled layer on the tensor cores:
 //
-//   down   S[M, r]  = Z[M, L] R[r, L]^T        T = X' A^T, and U = dY B from B^T
+//   down   S[M, r]  = Z[M, L] R                T = X' A^T (R = A^T), U = dY B (R = B)
 //   outer  G[C, r]  = Q[M, C]^T P[M, r]        dA^T from X' and s U, dB from dY and T
 //
 // Each reads a large bf16 matrix once and is bound by that read (r <= 128).  A
 // CTA sums a tile of 128 rows (tokens, or columns of Q) x r in tensor memory,
-// operands by TMA: for `down` both are K-major; for `outer` the contraction runs
-// over the rows of both, so a tile of 64 tokens x 64 columns lands as an MN-major
+// operands by TMA: Z and A are K-major; where the contraction runs over a
+// matrix's rows (Q, P, B) a tile of 64 rows x 64 columns lands as an MN-major
 // operand and the MMA transposes it (no transposed copy is made).  A cluster
 // splits the contraction over 2^log_splits CTAs, so that few rows still occupy
 // the GPU, and adds the partial sums through distributed shared memory in rank
@@ -69,19 +69,6 @@ struct Head {
 };
 static_assert(sizeof(Head) <= 1024, "stages begin at 1024");
 
-// MN-major operand with a 128-byte swizzle: 64 consecutive elements of a row are
-// 128 bytes, eight rows 1024 bytes (the stride between groups of the
-// contraction), the next 64 elements `group` bytes away.
-__device__ __forceinline__ uint64_t mn_desc(uint32_t addr, uint32_t group) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)(group >> 4) << 16;
-  d |= (uint64_t)(1024u >> 4) << 32;
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
-
 // Two results of a row, columns col and col + 1.
 template <bool OUTER>
 __device__ __forceinline__ void store2(const Args& g, const Problem& p, const float* v, int row, int col) {
@@ -136,7 +123,8 @@ __device__ __forceinline__ void store8(const Args& g, const Problem& p, const fl
   if (p.out && col < g.r) *reinterpret_cast<uint4*>(p.out + (int64_t)row * g.r + col) = pack8(v);
 }
 
-template <bool OUTER>
+// OUTER: both operands MN-major; RT (down): R [L, r] is.
+template <bool OUTER, bool RT>
 __global__ void __launch_bounds__(NUM_THREADS, 2)
 k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
             const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
@@ -194,11 +182,12 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
         if (OUTER) {
           tma_load_2d(a, tm_a, &S.full[s], row0, i * 64);
           tma_load_2d(a + 8192, tm_a, &S.full[s], row0 + 64, i * 64);
-          for (int j = 0; j * 8192 < g.b_bytes; ++j) tma_load_2d(b + j * 8192, tm_b, &S.full[s], j * 64, i * 64);
         } else {
           tma_load_2d(a, tm_a, &S.full[s], i * 64, row0);
-          tma_load_2d(b, tm_b, &S.full[s], i * 64, 0);
+          if (!RT) tma_load_2d(b, tm_b, &S.full[s], i * 64, 0);
         }
+        if (OUTER || RT)
+          for (int j = 0; j * 8192 < g.b_bytes; ++j) tma_load_2d(b + j * 8192, tm_b, &S.full[s], j * 64, i * 64);
         if (++s == NS) { s = 0; ph ^= 1; }
       }
       if (*abort) {                                // a wait gave up: let the copies in flight land
@@ -209,18 +198,20 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = idesc_bf16_f32(128, 16) + ((uint32_t)((g.N - 16) >> 3) << 17) +
-                             (OUTER ? (1u << 15) | (1u << 16) : 0u);
+                             (OUTER ? 1u << 15 : 0u) | (OUTER || RT ? 1u << 16 : 0u);
       int s = 0;
       uint32_t ph = 0;
       for (int i = k0; i < k1; ++i) {
         if (!mbar_wait(&S.full[s], ph, abort, g.status)) break;
         tc_fence_after();
         const uint32_t aa = smem_u32(stages + s * stage_bytes), bb = aa + A_BYTES;
-        const uint64_t a = OUTER ? mn_desc(aa, 8192) : sw128_kmajor_desc(aa);
-        const uint64_t b = OUTER ? mn_desc(bb, 8192) : sw128_kmajor_desc(bb);
-        constexpr uint32_t kStep = OUTER ? 2048 / 16 : 32 / 16;  // 16 rows, or 16 elements of a row
+        const uint64_t a = OUTER ? mx::mn_desc(aa, 8192) : sw128_kmajor_desc(aa);
+        const uint64_t b = OUTER || RT ? mx::mn_desc(bb, 8192) : sw128_kmajor_desc(bb);
+        constexpr uint32_t kRows = 2048 / 16, kElems = 32 / 16;  // 16 rows, or 16 elements of a row
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mma_ss(tmem, a + kStep * q, b + kStep * q, idesc, (i > k0 || q > 0) ? 1u : 0u);
+        for (int q = 0; q < 4; ++q)
+          mma_ss(tmem, a + (OUTER ? kRows : kElems) * q, b + (OUTER || RT ? kRows : kElems) * q, idesc,
+                 (i > k0 || q > 0) ? 1u : 0u);
         mma_commit(&S.empty[s]);
         if (++s == NS) { s = 0; ph ^= 1; }
       }
@@ -317,11 +308,11 @@ static void shape(Args& g, int num_sms) {
   g.ns = std::min(kMaxStages, budget / (A_BYTES + g.b_bytes));
 }
 
-template <bool OUTER>
+template <bool OUTER, bool RT>
 static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
                   const Args& g, bool dependent, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_devs{0};
-  set_smem_attr_once(k_mx_skinny<OUTER>, 224 * 1024, attr_devs);
+  set_smem_attr_once(k_mx_skinny<OUTER, RT>, 224 * 1024, attr_devs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(g.p[0].tiles + g.p[1].tiles) << g.log_splits, 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
@@ -336,13 +327,13 @@ static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMa
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = dependent ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_mx_skinny<OUTER>, a0, b0, a1, b1, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_mx_skinny<OUTER, RT>, a0, b0, a1, b1, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 }  // namespace skinny
 
-int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, float s, const float* row_scale,
-                   void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms) {
+int launch_mx_down(const void* Z, const void* R, bool r_rows, int M, int L, int r, int RP, float s,
+                   const float* row_scale, void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms) {
   using namespace skinny;
   Args g{};
   g.L = L;
@@ -351,11 +342,13 @@ int launch_mx_down(const void* Z, const void* R, int M, int L, int r, int RP, fl
   g.RP = RP;
   g.status = status;
   g.p[0] = Problem{M, (M + 127) / 128, row_scale, (__nv_bfloat16*)pad, (__nv_bfloat16*)out, 0, s};
-  g.b_bytes = g.N * 128;
+  g.b_bytes = r_rows ? (g.N + 63) / 64 * 8192 : g.N * 128;
   shape(g, num_sms);
   CUtensorMap a, b;
-  if (!make_tmap_2d_bf16(&a, Z, L, M, L, 64, 128) || !make_tmap_2d_bf16(&b, R, L, r, L, 64, g.N)) return QLORA_ERR_CUDA;
-  return launch<false>(a, b, a, b, g, dependent, st);
+  if (!make_tmap_2d_bf16(&a, Z, L, M, L, 64, 128) ||
+      !(r_rows ? make_tmap_2d_bf16(&b, R, r, L, r, 64, 64) : make_tmap_2d_bf16(&b, R, L, r, L, 64, g.N)))
+    return QLORA_ERR_CUDA;
+  return r_rows ? launch<false, true>(a, b, a, b, g, dependent, st) : launch<false, false>(a, b, a, b, g, dependent, st);
 }
 
 int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, const void* dY, int N, const void* T,
@@ -374,65 +367,39 @@ int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, co
   if (!make_tmap_2d_bf16(&a0, Xd, K, M, K, 64, 64) || !make_tmap_2d_bf16(&b0, sU, r, M, ldu, 64, 64) ||
       !make_tmap_2d_bf16(&a1, dY, N, M, N, 64, 64) || !make_tmap_2d_bf16(&b1, T, r, M, r, 64, 64))
     return QLORA_ERR_CUDA;
-  return launch<true>(a0, b0, a1, b1, g, false, st);
+  return launch<true, false>(a0, b0, a1, b1, g, false, st);
 }
 
 // ===========================================================================
-// The backward's transposed adapter factors, in one launch:
-//   At[K, RP] = A[r, K]^T, zero beyond r     Bt[r, N] = B[N, r]^T
-// A CTA a tile of 64 columns of A or rows of B, through shared memory; 16-byte
-// words of global memory on both sides, single elements in shared memory.
+// At[K, RP] = A[r, K]^T, zero beyond r, for the paired-SM GEMM and the masked term
+// of dX: a CTA 64 columns of A through shared memory, 16-byte words of global
+// memory on both sides.
 // ===========================================================================
 __global__ void __launch_bounds__(256)
-k_mx_transpose(const __nv_bfloat16* __restrict__ A, const __nv_bfloat16* __restrict__ B, int r, int K, int N, int RP,
-               __nv_bfloat16* __restrict__ At, __nv_bfloat16* __restrict__ Bt) {
-  __shared__ uint16_t tile[64][130];               // [column of A or row of B][row of A or column of B]
-  const int ka = (K + 63) / 64;
-  const int tid = threadIdx.x;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  if ((int)blockIdx.x < ka) {
-    const int k0 = blockIdx.x * 64;
-    for (int i = tid; i < RP * 8; i += 256) {
-      const int j = i >> 3, k = 8 * (i & 7);
-      const uint4 v = j < r && k0 + k < K ? *reinterpret_cast<const uint4*>(A + (int64_t)j * K + k0 + k) : zero;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+k_mx_transpose(const __nv_bfloat16* __restrict__ A, int r, int K, int RP, __nv_bfloat16* __restrict__ At) {
+  __shared__ uint16_t tile[64][130];               // [column of A][row of A]
+  const int tid = threadIdx.x, k0 = blockIdx.x * 64;
+  for (int i = tid; i < RP * 8; i += 256) {
+    const int j = i >> 3, k = 8 * (i & 7);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (j < r && k0 + k < K) v = *reinterpret_cast<const uint4*>(A + (int64_t)j * K + k0 + k);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) tile[k + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
-    __syncthreads();
-    for (int i = tid; i < 64 * (RP / 8); i += 256) {
-      const int k = i / (RP / 8), j = 8 * (i % (RP / 8));
-      if (k0 + k >= K) continue;
-      uint32_t w[4];
+    for (int e = 0; e < 8; ++e) tile[k + e][j] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+  }
+  __syncthreads();
+  for (int i = tid; i < 64 * (RP / 8); i += 256) {
+    const int k = i / (RP / 8), j = 8 * (i % (RP / 8));
+    if (k0 + k >= K) continue;
+    uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = tile[k][j + 2 * e] | (uint32_t)tile[k][j + 2 * e + 1] << 16;
-      *reinterpret_cast<uint4*>(At + (int64_t)(k0 + k) * RP + j) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
-    const int n0 = ((int)blockIdx.x - ka) * 64;
-    for (int i = tid; i < 64 * (r / 8); i += 256) {
-      const int n = i / (r / 8), j = 8 * (i % (r / 8));
-      const uint4 v = n0 + n < N ? *reinterpret_cast<const uint4*>(B + (int64_t)(n0 + n) * r + j) : zero;
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) tile[n][j + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-    }
-    __syncthreads();
-    for (int i = tid; i < r * 8; i += 256) {
-      const int j = i >> 3, n = 8 * (i & 7);
-      if (n0 + n >= N) continue;                   // N % 8 == 0
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = tile[n + 2 * e][j] | (uint32_t)tile[n + 2 * e + 1][j] << 16;
-      *reinterpret_cast<uint4*>(Bt + (int64_t)j * N + n0 + n) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    for (int e = 0; e < 4; ++e) w[e] = tile[k][j + 2 * e] | (uint32_t)tile[k][j + 2 * e + 1] << 16;
+    *reinterpret_cast<uint4*>(At + (int64_t)(k0 + k) * RP + j) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-void launch_mx_transpose(const void* A, const void* B, int r, int K, int N, int RP, void* At, void* Bt,
-                         cudaStream_t s) {
-  k_mx_transpose<<<(K + 63) / 64 + (N + 63) / 64, 256, 0, s>>>((const __nv_bfloat16*)A, (const __nv_bfloat16*)B, r, K, N,
-                                                               RP, (__nv_bfloat16*)At, (__nv_bfloat16*)Bt);
+void launch_mx_transpose(const void* A, int r, int K, int RP, void* At, cudaStream_t s) {
+  k_mx_transpose<<<(K + 63) / 64, 256, 0, s>>>((const __nv_bfloat16*)A, r, K, RP, (__nv_bfloat16*)At);
 }
 
 // ===========================================================================
