@@ -107,3 +107,42 @@ def test_it_is_the_layers_adapter_input(q):
     _, T = q.linear_fwd_dropout(w, X, A, B, 16.0, 0.2, 77)
     _, T2 = q.linear_fwd_dropout(w, q.dropout_fwd(X, 0.2, 77), A, B, 16.0, 0.0, 0)
     assert torch.equal(T, T2)
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits(q):
+    """More than 2^32 elements: the last rows equal the same rows with their number."""
+    M, K = 66000, 65544
+    X = torch.ones(M, K, dtype=torch.bfloat16, device="cuda")
+    Y = q.dropout_fwd(X, 0.5, 3)
+    assert torch.equal(Y[-9:], q.dropout_fwd(X[-9:].contiguous(), 0.5, 3, first=(M - 9) * K))
+    assert not torch.equal(Y[-9:], Y[:9])
+
+
+def test_captured_and_replayed(q):
+    X = make(40, 96, torch.bfloat16, 1).cuda()
+    Y = torch.empty_like(X)
+    q.qlora_dropout_fwd(X, 0.3, 8, Y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.qlora_dropout_fwd(X, 0.3, 8, Y)
+    X.mul_(3)
+    g.replay()
+    assert torch.equal(Y, q.dropout_fwd(X, 0.3, 8))
+
+
+def test_python_checks(q):
+    X = make(4, 8, torch.bfloat16, 1).cuda()
+    for bad in (X.t(), X.half(), X[0]):
+        with pytest.raises(ValueError):
+            q.dropout_fwd(bad, 0.1, 1)
+    with pytest.raises(ValueError):
+        q.dropout_fwd(X, 0.1, 1, residual=X.float())
+    with pytest.raises(ValueError):
+        q.dropout_fwd(X, 0.1, 1, residual=X[:2])
+    for p in (1.0, -0.1, float("nan")):
+        with pytest.raises(q.QLoraError):
+            q.dropout_fwd(X, p, 1)
+    with pytest.raises(q.QLoraError):
+        q.dropout_bwd(X, 0.1, 1, first=-1)
+    assert q.qlora_check_status() == 0

@@ -407,3 +407,186 @@ def test_python_checks(q):
     with pytest.raises(q.QLoraError):
         q.mx_linear_fwd(w, X, p=0.5)                          # dropout needs an adapter
     assert q.qlora_check_status() == 0
+
+
+# ---------------------------------------------------------------------------
+# Calls that the documentation allows at its edges
+# ---------------------------------------------------------------------------
+
+def layer_bounds(x, vx, vw, a, b, s, K):
+    """(Y in fp64, its bound) as in test_layer_forward_backward, no dropout."""
+    t = x @ a.T
+    y = vx @ vw.T + s * (t @ b.T)
+    ad = np.abs(x) @ np.abs(a).T
+    return y, (H * np.abs(y) + product_bound(vx, vw) + 1.01 * H * s * (np.abs(t) @ np.abs(b).T)
+               + (K + 130) * U * s * (ad @ np.abs(b).T))
+
+
+@pytest.mark.parametrize("M,N,K,r", [(5, 136, 192, 16), (40, 136, 192, 64), (200, 520, 320, 32), (1500, 40, 64, 8)])
+def test_layer_any_row_scale(q, M, N, K, r):
+    """A weight whose row scales are no powers of two (a tensor scale repeated,
+    say): the adapter's factor B / s may be rounded once more, deq(W) too."""
+    rng = np.random.default_rng(M)
+    w, vw = stored(q, N, K, mx.NVFP4, M, any_scale=True)
+    X, A = synth.activations(M, K, 1), synth.activations(r, K, 2, sigma=0.1)
+    B, dY = synth.activations(N, r, 3), synth.activations(M, N, 4)
+    Y, T = q.mx_linear_fwd(w, X.cuda(), A.cuda(), B.cuda(), 16.0)
+    dX, dA, dB = q.mx_linear_bwd(w, X.cuda(), dY.cuda(), A.cuda(), B.cuda(), 16.0, T=T)
+    assert q.qlora_check_status() == 0
+    x, a, b, d, s = f64(X), f64(A), f64(B), f64(dY), 16.0 / r
+    y, bound = layer_bounds(x, mx.fake_quantize(x, mx.NVFP4), vw, a, b, s, K)
+    within(Y, y, bound + 1.02 * H * s * (np.abs(x @ a.T) @ np.abs(b).T))
+    wb = mx.bf16(vw)                                    # what the backward multiplies by
+    u, ua = d @ b, np.abs(d) @ np.abs(b)
+    dx = d @ wb + s * (u @ a)
+    within(dX, dx, H * np.abs(dx) + N * U * (np.abs(d) @ np.abs(wb)) + s * (1.01 * H * (np.abs(u) @ np.abs(a))
+           + (N + 130) * U * (ua @ np.abs(a))))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_wide_tokens(q, fmt):
+    """A contraction past what one pass of the token kernel holds in registers."""
+    M, N, K, r = 3, 72, 24640, 8
+    X, A, B, w, vw = layer(q, fmt, M, N, K, r, 9)
+    Y, T = q.mx_linear_fwd(w, X.cuda(), A.cuda(), B.cuda(), 16.0)
+    x = f64(X)
+    y, bound = layer_bounds(x, mx.fake_quantize(x, fmt), vw, f64(A), f64(B), 2.0, K)
+    within(Y, y, bound)
+    t = x @ f64(A).T
+    within(T, t, H * np.abs(t) + K * U * (np.abs(x) @ np.abs(f64(A)).T))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", [1, 30, 60, 300])
+def test_zero_and_nan_tokens_stay_in_their_rows(q, fmt, M):
+    """A zero token gives zeros, a NaN token NaNs, and neither touches the rest."""
+    N, K, r = 264, 576, 16
+    X, A, B, w, _ = layer(q, fmt, M + 2, N, K, r, 21)
+    X, A, B = X.cuda(), A.cuda(), B.cuda()
+    Y, T = q.mx_linear_fwd(w, X, A, B, 16.0)
+    Z = X.clone()
+    Z[M // 2], Z[M] = 0, float("nan")
+    P, S = q.mx_linear_fwd(w, Z, A, B, 16.0)
+    assert q.qlora_check_status() == q._lib.QLORA_ERR_NONFINITE
+    keep = torch.ones(M + 2, dtype=torch.bool, device="cuda")
+    keep[M // 2] = keep[M] = False
+    assert torch.equal(P[keep], Y[keep]) and torch.equal(S[keep], T[keep])
+    assert bool((P[M // 2] == 0).all()) and bool((S[M // 2] == 0).all())
+    assert bool(P[M].isnan().all()) and bool(S[M].isnan().all())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_zero_weight_rows(q, fmt):
+    """Rows of zeros in W leave the adapter's term alone, forward and backward."""
+    M, N, K, r = 20, 136, 256, 16
+    W = synth.weight(N, K, 1)
+    W[8:80] = 0
+    X, A, B = synth.activations(M, K, 2), synth.activations(r, K, 3, sigma=0.02), synth.activations(N, r, 4)
+    w = q.mx_quantize(W.cuda(), fmt)
+    for m in (M, 1):
+        Y, T = q.mx_linear_fwd(w, X[:m].cuda(), A.cuda(), B.cuda(), 16.0)
+        y = f64(X[:m]) @ f64(A).T @ f64(B).T
+        bound = 4 * H * (np.abs(f64(X[:m]) @ f64(A).T) @ np.abs(f64(B)).T)
+        got = f64(Y)[:, 8:80]
+        assert np.all(np.abs(got - y[:, 8:80]) <= bound[:, 8:80])
+
+
+def test_the_same_bits_every_time(q):
+    """Split contractions add in a fixed order: ten runs, one result."""
+    for M, N, K, r in ((1, 264, 4096, 16), (24, 520, 2048, 8), (100, 136, 8192, 64), (300, 1024, 512, 16)):
+        X, A, B, w, _ = layer(q, mx.NVFP4, M, N, K, r, 5)
+        X, A, B, dY = X.cuda(), A.cuda(), B.cuda(), synth.activations(M, N, 6).cuda()
+        first = None
+        for _ in range(10):
+            Y, T = q.mx_linear_fwd(w, X, A, B, 16.0, p=0.0)
+            out = (Y, T) + q.mx_linear_bwd(w, X, dY, A, B, 16.0, T=T)
+            if first is None:
+                first = out
+            assert all(torch.equal(a, b) for a, b in zip(first, out))
+
+
+def test_two_streams_at_once(q):
+    """Calls that overlap on two streams, each with its own buffers."""
+    parts = []
+    for i, (M, fmt) in enumerate(((20, mx.NVFP4), (20, mx.MXFP4), (700, mx.NVFP4), (150, mx.MXFP4))):
+        X, A, B, w, _ = layer(q, fmt, M, 520, 1024, 16, 30 + i)
+        X, A, B, dY = X.cuda(), A.cuda(), B.cuda(), synth.activations(M, 520, i).cuda()
+        Y, T = q.mx_linear_fwd(w, X, A, B, 16.0, p=0.1, seed=i)
+        want = (Y, T) + q.mx_linear_bwd(w, X, dY, A, B, 16.0, p=0.1, seed=i, T=T)
+        parts.append((X, A, B, dY, w, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in parts]
+    got = []
+    for rep in range(3):
+        for i, (X, A, B, dY, w, want) in enumerate(parts):
+            Y, T = q.mx_linear_fwd(w, X, A, B, 16.0, p=0.1, seed=i, stream=streams[i])
+            got.append((i, (Y, T) + q.mx_linear_bwd(w, X, dY, A, B, 16.0, p=0.1, seed=i, T=T, stream=streams[i])))
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(a, b) for a, b in zip(parts[i][5], out))
+    assert q.qlora_check_status() == 0
+
+
+@pytest.mark.parametrize("M", [20, 200])
+def test_backward_in_a_graph(q, M):
+    """The backward captured and replayed on new gradients."""
+    X, A, B, w, _ = layer(q, mx.MXFP4, M, 264, 448, 16, 5)
+    X, A, B = X.cuda(), A.cuda(), B.cuda()
+    dY = synth.activations(M, 264, 1).cuda()
+    out = [torch.empty_like(t) for t in (X, A, B)]
+    n = q.workspace_bytes(q._lib.QLORA_OP_MX_BWD_DROPOUT, M, 264, 448, 16)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    q.qlora_mx_linear_bwd(w, X, dY, A, B, 16.0, *out, p=0.2, seed=4, ws=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        q.qlora_mx_linear_bwd(w, X, dY, A, B, 16.0, *out, p=0.2, seed=4, ws=ws)
+    for i in range(3):
+        dY.copy_(synth.activations(M, 264, 10 + i))
+        g.replay()
+        want = q.mx_linear_bwd(w, X, dY, A, B, 16.0, p=0.2, seed=4)
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", [(16, 4096, 4096), (70, 1024, 4096), (130, 2048, 1024), (600, 1024, 2048),
+                                   (2100, 512, 1024), (33, 264, 8192)])
+def test_larger_layers_by_their_norm(q, fmt, M, N, K):
+    """Sizes that reach every kernel of the layer, against fp64 products on the
+    GPU of the tensors' own dequantised values: the bf16 roundings are
+    independent, so the error's norm is below half a step of the result's."""
+    r, s = 16, 1.0
+    X, A, B, w, _ = layer(q, fmt, M, N, K, r, M + K)
+    X, A, B, dY = X.cuda(), A.cuda(), B.cuda(), synth.activations(M, N, 9).cuda()
+    Y, T = q.mx_linear_fwd(w, X, A, B, 16.0)
+    dX, dA, dB = q.mx_linear_bwd(w, X, dY, A, B, 16.0, T=T)
+    vw, vx = q.mx_dequantize(w).double(), q.mx_dequantize(q.mx_quantize(X, fmt)).double()
+    x, a, b, d = X.double(), A.double(), B.double(), dY.double()
+    u = d @ b
+    for got, ref in ((Y, vx @ vw.T + s * (x @ a.T) @ b.T), (T, x @ a.T), (dX, d @ vw + s * u @ a),
+                     (dA, s * u.T @ x), (dB, s * d.T @ T.double())):
+        assert float((got.double() - ref).norm()) <= H * float(ref.norm())
+    assert q.qlora_check_status() == 0
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("fmt", FMTS)
+def test_offsets_past_32_bits(q, fmt):
+    """More than 2^32 elements quantised and dequantised, more than 2^31 outputs
+    of a product: the last rows equal the same rows on their own."""
+    rows, K = 66000, 65536
+    g = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.empty(rows, K, dtype=torch.bfloat16, device="cuda")
+    X.zero_()
+    X[-256:] = torch.randn(256, K, generator=g, device="cuda")
+    t = q.mx_quantize(X, fmt)
+    tail = q.mx_quantize(X[-256:].contiguous(), fmt)
+    assert torch.equal(t.packed.view(rows, -1)[-256:], tail.packed.view(256, -1))
+    assert torch.equal(q.mx_dequantize(t)[-256:], q.mx_dequantize(tail))
+    del X
+    one = q.mx_quantize(torch.randn(3, K, generator=g, device="cuda"), fmt)
+    assert torch.equal(q.mx_matmul(t, one)[-256:], q.mx_matmul(tail, one))
+    del t
+    w = q.mx_quantize(torch.randn(60000, 64, generator=g, device="cuda"), fmt)
+    x = torch.randn(40000, 64, generator=g, device="cuda")
+    Y = q.mx_matmul(q.mx_quantize(x, fmt), w)
+    assert torch.equal(Y[-200:], q.mx_matmul(q.mx_quantize(x[-200:].contiguous(), fmt), w))
