@@ -106,6 +106,31 @@ def test_quantise_edges(q, fmt, dtype):
     check_quantised(q, torch.stack(rows).cuda(), fmt)
 
 
+@pytest.mark.parametrize("k", [0, -40, 90])
+def test_midpoints_under_every_block_scale(q, k):
+    """The seven midpoints and the floats on both sides of each, under all 126 E4M3 scales."""
+    S = torch.arange(1, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()[:, None]
+    t = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]) * S            # exact: 4 and 3 bits
+    X = torch.zeros(126, 64)
+    X[:, 0] = 2688.0                                                         # the row scale is 2^k
+    X[:, 16] = X[:, 32] = X[:, 48] = (6 * S)[:, 0]
+    X[:, 17:24] = t
+    X[:, 33:40] = torch.nextafter(t, torch.full_like(t, 1e30))
+    X[:, 49:56] = -torch.nextafter(t, torch.zeros_like(t))
+    codes, scale, s = mx.quantize(X.double().numpy() * 2.0 ** k, mx.NVFP4)
+    assert np.all(s == 2.0 ** k) and np.all(scale[:, 1:4] == np.arange(1, 127)[:, None])
+    check_quantised(q, (X * 2.0 ** k).cuda(), mx.NVFP4)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(300, 32), (1, 96), (129, 224), (257, 480), (130, 544), (40, 20480), (33, 26624)])
+def test_quantise_row_lengths(q, fmt, dtype, rows, cols):
+    """Rows that share a CTA, a warp or part of one, and rows longer than a CTA's registers."""
+    X = torch.randn(rows, cols, generator=torch.Generator().manual_seed(cols))
+    check_quantised(q, (X * torch.logspace(-12, 12, rows)[:, None]).to(dtype).cuda(), fmt)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
