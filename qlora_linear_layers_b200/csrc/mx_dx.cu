@@ -16,11 +16,14 @@
 //    stages ahead (one group alone: 1000 cycles a stage, its chain of loads,
 //    conversion and fence).
 //  * a cluster splits the contraction over 2^log_splits CTAs and adds the partial
-//    sums through distributed shared memory in rank order.
+//    sums through distributed shared memory in rank order; or, unsplit, is a pair of
+//    SMs (tcgen05 cta_group::2) with a tile of 256 columns x 256 tokens, each
+//    expanding its own 128 columns and loading half of the tokens.
 //
 // Bound: a stage is 4 (45 + BN / 2) cycles of MMA (692 at 256 tokens), about 400
 // of converter issue, and at 256 tokens 96 KB of shared-memory traffic (750
-// cycles).  Every tile of tokens expands the weight again, so from some token count
+// cycles; 64 KB in a pair: W 18944 x 3584, 1111 tokens 140 us against 150, 470 ns a
+// stage at the clock that the tensor cores' power leaves).  Every tile of tokens expands the weight again, so from some token count
 // on the expansion to HBM and the paired-SM GEMM are cheaper (dx_cost).
 // Every wait is bounded (QLORA_ERR_TIMEOUT).
 
@@ -58,16 +61,20 @@ struct DxArgs {
   int* status;
 };
 
-template <int BN>
+// PAIR: two CTAs on paired SMs share a tile of 256 columns x BN tokens, each with
+// its 128 columns of W and half of the tokens.
+template <int BN, bool PAIR>
 struct Shape {
-  static constexpr int B_BYTES = BN * 128;
-  static constexpr int NS = BN > 128 ? 4 : 6;
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int B_ROWS = BN / kCtas;        // tokens of a CTA's loads
+  static constexpr int B_BYTES = B_ROWS * 128;
+  static constexpr int NS = B_ROWS > 128 ? 4 : 6;
   static constexpr int D_COLS = BN < 32 ? 32 : BN;
 };
 
-template <int BN>
+template <int BN, bool PAIR>
 struct Smem {
-  using Sh = Shape<BN>;
+  using Sh = Shape<BN, PAIR>;
   uint8_t a[Sh::NS][A_BYTES];                      // a, then b: the partial sums of the reduction
   uint8_t b[Sh::NS][Sh::B_BYTES];
   uint8_t out[4][2][kChunk * 64];                  // an epilogue warp's chunks
@@ -76,30 +83,32 @@ struct Smem {
   int abort;
 };
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool PAIR>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf16
         const __grid_constant__ CUtensorMap tm_a,          // [r, K] bf16
         const __grid_constant__ CUtensorMap tm_su,         // [M, RP] bf16
         const __grid_constant__ CUtensorMap tm_out,        // [M, K] bf16
         const DxArgs g) {
-  using Sh = Shape<BN>;
-  constexpr int NS = Sh::NS;
+  using Sh = Shape<BN, PAIR>;
+  constexpr int NS = Sh::NS, P = Sh::kCtas;
   static_assert(BN * 512 <= NS * (A_BYTES + Sh::B_BYTES), "reduction buffer");
   extern __shared__ uint8_t smem_raw[];
-  Smem<BN>& S = *smem_align1024<Smem<BN>>(smem_raw);
+  Smem<BN, PAIR>& S = *smem_align1024<Smem<BN, PAIR>>(smem_raw);
   const Args& p = g.out;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ls = g.log_splits, splits = 1 << ls;
-  const int rank = (int)cluster_ctarank();
-  const int c0 = (int)(blockIdx.x >> ls) * 128, m0 = (int)blockIdx.y * BN;    // columns of W, tokens
+  const int ls = PAIR ? 0 : g.log_splits, splits = 1 << ls;
+  const int half = PAIR ? (int)cluster_ctarank() : 0, rank = PAIR ? 0 : (int)cluster_ctarank();
+  const bool leader = half == 0;
+  const int c0 = (int)(blockIdx.x >> ls) * 128;                              // columns of W
+  const int m0 = (int)blockIdx.y * BN, mb = m0 + half * Sh::B_ROWS;          // tokens
   const int nk_all = (g.rows + 63) / 64;
   const int k0 = (int)(((int64_t)nk_all * rank) >> ls), k1 = (int)(((int64_t)nk_all * (rank + 1)) >> ls);
   const int na = rank == 0 ? g.na : 0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&S.full_a[i], kConv);
+      mbar_init(&S.full_a[i], P * kConv);          // a pair's: the leader's, for both
       mbar_init(&S.full_b[i], 1);
       mbar_init(&S.empty[i], 1);
     }
@@ -108,60 +117,80 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&S.tmem_base, Sh::D_COLS);
-    tmem_relinquish();
+    if (PAIR) {
+      tmem_alloc_pair(&S.tmem_base, Sh::D_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(&S.tmem_base, Sh::D_COLS);
+      tmem_relinquish();
+    }
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tm_dy);
     tma_prefetch_desc(&tm_out);
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();                        // barriers of both CTAs initialised
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   volatile int* abort = &S.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return PAIR ? mbar_wait_cluster(bar, parity, abort, g.status) : mbar_wait(bar, parity, abort, g.status);
+  };
+  auto load_tile = [&](void* dst, const CUtensorMap* t, uint64_t* bar, int x, int y) {
+    if (PAIR) tma_load_2d_pair(dst, t, mapa_shared(smem_u32(bar), 0), x, y);
+    else tma_load_2d(dst, t, bar, x, y);
+  };
+  auto commit = [&](uint64_t* bar) {
+    if (PAIR) mma_commit_pair_mc(bar, 0x3);
+    else mma_commit(bar);
+  };
 
   if (warp == 0) {
     if (elect_one()) {
       int s = 0, i = -na;
       uint32_t ph = 0;
       for (; i < k1 - k0; ++i) {
-        if (!mbar_wait(&S.empty[s], ph ^ 1, abort, g.status)) break;
+        if (!wait(&S.empty[s], ph ^ 1)) break;
         if (i < 0) {
-          mbar_arrive_expect_tx(&S.full_b[s], A_BYTES + Sh::B_BYTES);
-          tma_load_2d(S.a[s], &tm_a, &S.full_b[s], c0, (i + na) * 64);
-          tma_load_2d(S.a[s] + 8192, &tm_a, &S.full_b[s], c0 + 64, (i + na) * 64);
-          tma_load_2d(S.b[s], &tm_su, &S.full_b[s], (i + na) * 64, m0);
+          if (leader) mbar_arrive_expect_tx(&S.full_b[s], P * (A_BYTES + Sh::B_BYTES));
+          load_tile(S.a[s], &tm_a, &S.full_b[s], c0, (i + na) * 64);
+          load_tile(S.a[s] + 8192, &tm_a, &S.full_b[s], c0 + 64, (i + na) * 64);
+          load_tile(S.b[s], &tm_su, &S.full_b[s], (i + na) * 64, mb);
         } else {
-          mbar_arrive_expect_tx(&S.full_b[s], Sh::B_BYTES);
-          tma_load_2d(S.b[s], &tm_dy, &S.full_b[s], (k0 + i) * 64, m0);
+          if (leader) mbar_arrive_expect_tx(&S.full_b[s], P * Sh::B_BYTES);
+          load_tile(S.b[s], &tm_dy, &S.full_b[s], (k0 + i) * 64, mb);
         }
         if (++s == NS) { s = 0; ph ^= 1; }
       }
-      if (*abort) {                                // a wait gave up: let the copies in flight land
+      if (!PAIR && *abort) {                       // a wait gave up: let the copies in flight land
         const int n = na + i;
         for (int j = max(0, n - NS); j < n; ++j) drain_wait(&S.full_b[j % NS], (j / NS) & 1, g.status);
       }
     }
   } else if (warp == 1) {
-    if (elect_one()) {
-      constexpr uint32_t idesc = idesc_bf16_f32(128, BN) | (1u << 15);       // A is MN-major
+    if (leader && elect_one()) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128 * P, BN) | (1u << 15);   // A is MN-major
       int s = 0;
       uint32_t ph = 0;
       for (int i = -na; i < k1 - k0; ++i) {
-        if (!mbar_wait(&S.full_b[s], ph, abort, g.status)) break;
+        if (!wait(&S.full_b[s], ph)) break;
         // the converters never fill the first na slots' first use (na <= 2 < NS)
-        if (i >= 0 && !mbar_wait(&S.full_a[s], ph ^ (s < na ? 1u : 0u), abort, g.status)) break;
+        if (i >= 0 && !wait(&S.full_a[s], ph ^ (s < na ? 1u : 0u))) break;
         tc_fence_after();
         const uint64_t a = mn_desc(smem_u32(S.a[s]), 8192), b = sw128_kmajor_desc(smem_u32(S.b[s]));
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          mma_ss(tmem, a + 128 * q, b + 2 * q, idesc, (i > -na || q > 0) ? 1u : 0u);
-        mma_commit(&S.empty[s]);
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t add = (i > -na || q > 0) ? 1u : 0u;
+          if (PAIR) mma_ss_pair(tmem, a + 128 * q, b + 2 * q, idesc, add);
+          else mma_ss(tmem, a + 128 * q, b + 2 * q, idesc, add);
+        }
+        commit(&S.empty[s]);
         if (++s == NS) { s = 0; ph ^= 1; }
       }
-      mma_commit(&S.acc_full);
-      mbar_wait(&S.acc_full, 0, abort, g.status);
+      commit(&S.acc_full);
+      wait(&S.acc_full, 0);
     }
   } else if (warp >= 6) {
     // thread (row, q): columns 32 q .. 32 q + 31 of the tile's row, one of a warp's 32
@@ -209,7 +238,7 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
         v[2] = mx_values8<FMT>(cw[d].z, s1, rs[d]);
         v[3] = mx_values8<FMT>(cw[d].w, s1, rs[d]);
         load(i + kGroups * kAhead, d);
-        if (lane == 0) ok = mbar_wait(&S.empty[s], ph ^ 1, abort, g.status);
+        if (lane == 0) ok = wait(&S.empty[s], ph ^ 1);
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (!ok) break;
 #pragma unroll
@@ -217,17 +246,27 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
           *reinterpret_cast<uint4*>(S.a[s] + base + ((((q & 1) * 4 + j) ^ (row & 7)) << 4)) = v[j];
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.full_a[s]);
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&S.full_a[s]), 0));
+          else mbar_arrive(&S.full_a[s]);
+        }
         if ((s += kGroups) >= NS) { s -= NS; ph ^= 1; }
       }
     }
   } else {
-    mbar_wait(&S.acc_full, 0, abort, g.status);
+    wait(&S.acc_full, 0);
   }
   __syncwarp();
+  if (PAIR && warp == 0 && lane == 0 && *abort) {
+    // a wait gave up: the copies in flight count on barriers that may never
+    // complete, so give them a millisecond to land
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) {
+    }
+  }
   const int quad = warp & 3;
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-  if (ls == 0) {
+  if (PAIR || ls == 0) {
     if (warp >= 2 && warp < 6) {
       tc_fence_after();
       const int e = warp - 2, cw0 = c0 + quad * 32;
@@ -294,10 +333,12 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if (PAIR) cluster_sync();                        // both CTAs done with the paired TMEM
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, Sh::D_COLS);
+    if (PAIR) tmem_dealloc_pair(tmem, Sh::D_COLS);
+    else tmem_dealloc(tmem, Sh::D_COLS);
   }
 }
 
@@ -306,17 +347,20 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
 // B200 to W 4096 x 4096, 18944 x 3584, 3584 x 18944 and 1024 x 1024 with 16 to 1111
 // tokens, e.g. W 18944 x 3584: 33 us (16 tokens), 42 (128), 45 (256), 78 (512), 147
 // (1111), against 127, 127, 128, 130 and 140 us by way of HBM.
-static int64_t cost(int M, int N, int K, int na, int num_sms, int* bn, int* log_splits) {
-  const int widths[5] = {16, 32, 64, 128, 256}, stage[5] = {38, 38, 40, 46, 50}, join[5] = {80, 150, 220, 350, 870};
+static int64_t cost(int M, int N, int K, int na, int num_sms, int* bn, bool* pair, int* log_splits) {
+  constexpr int kShapes = 6;                       // the last: paired SMs
+  const int widths[kShapes] = {16, 32, 64, 128, 256, 256}, stage[kShapes] = {38, 38, 40, 46, 50, 46},
+            join[kShapes] = {80, 150, 220, 350, 870, 0};
   const int nk = (N + 63) / 64;
   int64_t best = INT64_MAX;
-  for (int i = M > 16 ? 1 : 0; i < 5; ++i) {       // a chunk of output is 32 tokens: 16 only by itself
-    const int64_t tiles = (int64_t)((K + 127) / 128) * ((M + widths[i] - 1) / widths[i]);
-    for (int s = 0; s <= 3 && (nk >> s) >= 4; ++s) {
+  for (int i = M > 16 ? 1 : 0; i < kShapes; ++i) { // a chunk of output is 32 tokens: 16 only by itself
+    const bool two = i == kShapes - 1;
+    const int64_t tiles = (two ? (K + 255) / 256 * 2 : (K + 127) / 128) * (int64_t)((M + widths[i] - 1) / widths[i]);
+    for (int s = 0; s <= (two ? 0 : 3) && (nk >> s) >= 4; ++s) {
       if (s && (tiles << s) > num_sms + num_sms / 8) break;
       const int64_t waves = s ? 1 : (tiles + num_sms - 1) / num_sms;
       const int64_t c = 400 + waves * (na + (nk + (1 << s) - 1) / (1 << s)) * stage[i] + (s ? join[i] : 0);
-      if (c < best) { best = c; *bn = widths[i]; *log_splits = s; }
+      if (c < best) { best = c; *bn = widths[i]; *pair = two; *log_splits = s; }
     }
   }
   return best;
@@ -331,47 +375,51 @@ static int64_t cost_expanded(int M, int N, int K, int na, int num_sms) {
   return 900 + (int64_t)N * K * 26 / 400000 + rounds * (na + (N + 63) / 64) * 35;
 }
 
-template <int FMT, int BN>
+template <int FMT, int BN, bool PAIR>
 static int launch(const qlora_mx_tensor* w, const void* dY, const void* A, int r, const void* sU, int RP, DxArgs g,
                   cudaStream_t s) {
+  using Sh = Shape<BN, PAIR>;
   CUtensorMap ty, ta, tu, to;
   const int M = g.out.M, K = g.out.N;
-  if (!make_tmap_2d_bf16(&ty, dY, g.rows, M, g.rows, 64, BN) || !make_tmap_store_bf16(&to, g.out.out, K, M, kChunk))
+  if (!make_tmap_2d_bf16(&ty, dY, g.rows, M, g.rows, 64, Sh::B_ROWS) || !make_tmap_store_bf16(&to, g.out.out, K, M, kChunk))
     return QLORA_ERR_CUDA;
   ta = ty;
   tu = ty;
-  if (g.na && (!make_tmap_2d_bf16(&ta, A, K, r, K, 64, 64) || !make_tmap_2d_bf16(&tu, sU, RP, M, RP, 64, BN)))
+  if (g.na && (!make_tmap_2d_bf16(&ta, A, K, r, K, 64, 64) || !make_tmap_2d_bf16(&tu, sU, RP, M, RP, 64, Sh::B_ROWS)))
     return QLORA_ERR_CUDA;
-  constexpr size_t bytes = sizeof(Smem<BN>) + 1024;
+  constexpr size_t bytes = sizeof(Smem<BN, PAIR>) + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
   static std::atomic<unsigned long long> attr_devs{0};
-  set_smem_attr_once(k_mx_dx<FMT, BN>, (int)bytes, attr_devs);
+  set_smem_attr_once(k_mx_dx<FMT, BN, PAIR>, (int)bytes, attr_devs);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((K + 127) / 128) << g.log_splits, (unsigned)((M + BN - 1) / BN), 1);
+  constexpr int cols = 128 * Sh::kCtas;
+  cfg.gridDim = dim3((unsigned)((K + cols - 1) / cols * Sh::kCtas) << g.log_splits, (unsigned)((M + BN - 1) / BN), 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1u << g.log_splits;
+  attr[0].val.clusterDim.x = (unsigned)Sh::kCtas << g.log_splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_mx_dx<FMT, BN>, ty, ta, tu, to, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_mx_dx<FMT, BN, PAIR>, ty, ta, tu, to, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 template <int FMT>
 static int launch_fmt(const qlora_mx_tensor* w, const void* dY, const void* A, int r, const void* sU, int RP, DxArgs g,
                       cudaStream_t s, int num_sms) {
   int bn = 0;
-  cost(g.out.M, g.rows, g.out.N, g.na, num_sms, &bn, &g.log_splits);
+  bool pair = false;
+  cost(g.out.M, g.rows, g.out.N, g.na, num_sms, &bn, &pair, &g.log_splits);
+  if (pair) return launch<FMT, 256, true>(w, dY, A, r, sU, RP, g, s);
   switch (bn) {
-    case 16: return launch<FMT, 16>(w, dY, A, r, sU, RP, g, s);
-    case 32: return launch<FMT, 32>(w, dY, A, r, sU, RP, g, s);
-    case 64: return launch<FMT, 64>(w, dY, A, r, sU, RP, g, s);
-    case 128: return launch<FMT, 128>(w, dY, A, r, sU, RP, g, s);
-    default: return launch<FMT, 256>(w, dY, A, r, sU, RP, g, s);
+    case 16: return launch<FMT, 16, false>(w, dY, A, r, sU, RP, g, s);
+    case 32: return launch<FMT, 32, false>(w, dY, A, r, sU, RP, g, s);
+    case 64: return launch<FMT, 64, false>(w, dY, A, r, sU, RP, g, s);
+    case 128: return launch<FMT, 128, false>(w, dY, A, r, sU, RP, g, s);
+    default: return launch<FMT, 256, false>(w, dY, A, r, sU, RP, g, s);
   }
 }
 
@@ -379,7 +427,8 @@ static int launch_fmt(const qlora_mx_tensor* w, const void* dY, const void* A, i
 
 bool mx_dx_expands_inside(int M, int N, int K, int na, int num_sms) {
   int bn, ls;
-  return N >= 256 && dx::cost(M, N, K, na, num_sms, &bn, &ls) <= dx::cost_expanded(M, N, K, na, num_sms);
+  bool pair;
+  return N >= 256 && dx::cost(M, N, K, na, num_sms, &bn, &pair, &ls) <= dx::cost_expanded(M, N, K, na, num_sms);
 }
 
 int launch_mx_dx(const qlora_mx_tensor* w, const void* dY, int M, const void* A, int r, const void* sU, int RP, int na,
