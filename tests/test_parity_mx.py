@@ -574,8 +574,8 @@ def test_backward_in_a_graph(q, M):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("M,N,K", [(16, 4096, 4096), (70, 1024, 4096), (130, 2048, 1024), (600, 1024, 2048),
-                                   (2100, 512, 1024), (33, 264, 8192), (1111, 320, 2464), (777, 2048, 3488),
-                                   (250, 4096, 4000)])
+                                   (2100, 512, 1024), (33, 264, 8192), (1111, 320, 2432), (777, 2048, 3520),
+                                   (250, 4096, 4032)])
 def test_larger_layers_by_their_norm(q, fmt, M, N, K):
     """Sizes that reach every kernel of the layer, against fp64 products on the
     GPU of the tensors' own dequantised values: the bf16 roundings are
