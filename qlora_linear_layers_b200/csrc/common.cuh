@@ -350,6 +350,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launches
+// ---------------------------------------------------------------------------
+// The next grid, if it was launched as a dependent, may start once every CTA of
+// this one has passed here; it waits for this grid's end where it needs it.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Wait for the grid that this one was launched after (returns at once when the
+// launch had no such attribute).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Thread-block clusters and the paired-SM (cta_group::2) forms
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -111,6 +111,7 @@ template <typename T, bool RES, bool DENSE>
 __global__ void __launch_bounds__(256)
 k_dropout8(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, int64_t blocks, int64_t row_blocks,
            int tail, int64_t first_block, const __grid_constant__ DropoutKeys d) {
+  grid_launch_dependents();
   const int64_t step = (int64_t)gridDim.x * blockDim.x;
   for (int64_t b = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; b < blocks; b += kUnroll * step) {
     Oct<T> x[kUnroll], r[kUnroll];
@@ -159,13 +160,13 @@ k_dropout8(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, 
 
 template <typename T>
 static void launch_dropout_t(const T* X, int64_t ldx, const T* R, int64_t ldr, T* Y, int64_t ldy, int64_t rows,
-                             int64_t cols, int64_t first, const Dropout& drop, cudaStream_t s) {
+                             int64_t cols, int64_t first, const Dropout& drop, int per_sm, cudaStream_t s) {
   const DropoutKeys d = make_keys(drop);
   const int64_t n = rows * cols;
   const int64_t blocks = (n + 14) / 8;
   const bool dense = (ldx == cols && ldy == cols && (!R || ldr == cols)) || rows == 1;
   if (first % 8 == 0 && (dense || (cols | ldx | ldy | (R ? ldr : 0)) % 8 == 0)) {
-    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n / 8 + 511) / 512, 148 * 8));
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n / 8 + 511) / 512, 148 * per_sm));
     auto run = [&](auto kern) {
       kern<<<grid, 256, 0, s>>>(X, ldx, R, ldr, Y, ldy, n / 8, cols / 8, (int)(n % 8), first / 8, d);
     };
@@ -183,12 +184,12 @@ static void launch_dropout_t(const T* X, int64_t ldx, const T* R, int64_t ldr, T
 }
 
 void launch_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, void* Y, int64_t ldy, int dtype,
-                    int64_t rows, int64_t cols, int64_t first, const Dropout& d, cudaStream_t s) {
+                    int64_t rows, int64_t cols, int64_t first, const Dropout& d, cudaStream_t s, int per_sm) {
   if (dtype == QLORA_F32)
-    launch_dropout_t((const float*)X, ldx, (const float*)R, ldr, (float*)Y, ldy, rows, cols, first, d, s);
+    launch_dropout_t((const float*)X, ldx, (const float*)R, ldr, (float*)Y, ldy, rows, cols, first, d, per_sm, s);
   else
     launch_dropout_t((const __nv_bfloat16*)X, ldx, (const __nv_bfloat16*)R, ldr, (__nv_bfloat16*)Y, ldy, rows, cols,
-                     first, d, s);
+                     first, d, per_sm, s);
 }
 
 }  // namespace qnf4

@@ -34,10 +34,15 @@ void launch_merge(const nf4_weight* w, const void* A, const void* B, int r, floa
                   cudaStream_t st);
 
 struct Dropout;
+// CTAs of the dropout an SM, and how many where other kernels run beside it: five
+// take 1280 of an SM's threads and 40 of its 64 K registers (four to six measure
+// alike).
+constexpr int kDropoutAlone = 8, kDropoutBeside = 5;
+
 // Y = RN(RN32(D c X) + R) over [rows, cols] with leading dimensions ldx, ldr,
 // ldy (R may be null); element (i, j) has number first + i * cols + j.
 void launch_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, void* Y, int64_t ldy, int dtype,
-                    int64_t rows, int64_t cols, int64_t first, const Dropout& d, cudaStream_t s);
+                    int64_t rows, int64_t cols, int64_t first, const Dropout& d, cudaStream_t s, int per_sm = kDropoutAlone);
 
 // All argument checks of qlora_linear_fwd except the workspace (capi.cu).
 int validate_fwd_args(const nf4_weight* w, const void* X, int64_t M, const void* A, const void* B,

@@ -22,8 +22,10 @@ __host__ __device__ constexpr int64_t mx_scale_offset(int64_t r, int64_t c, int6
   return ((r >> 7) * tiles + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
 }
 
+// beside: launched beside the kernel before it, of which it reads nothing, and
+// ending after it.
 void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
-                        uint8_t* packed, uint8_t* scales, float* row_scale, int* status,
+                        uint8_t* packed, uint8_t* scales, float* row_scale, bool beside, int* status,
                         cudaStream_t s);
 struct Dropout;
 // dX [M, K] (bf16, in place) += D c (sU [M, RP] At [K, RP]^T), K % 64 == 0.
@@ -68,18 +70,20 @@ bool mx_adapter_in_epilogue(int M, int N, int K, int num_sms);
 
 // Y[M, N] = deq(x) deq(w)^T + the adapter's term.  after_prep: launched as the
 // dependent of the kernel before it (launch_mx_prep, launch_mx_quantize or
-// launch_mx_down), which is the last that writes x, sT or tok; w and its adapter
-// factor were complete before that one began.  QLORA_OK or QLORA_ERR_CUDA.
+// launch_mx_down), with whose end x, sT and tok are complete; w and its adapter
+// factor were before that one began.  QLORA_OK or QLORA_ERR_CUDA.
 int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
                    int* status, cudaStream_t s, int num_sms);
 
 // With S = Z R^T, Z [M, L] and R [r, L] (r_rows: R^T [L, r]) bf16: pad [M, RP] = RNbf16(s S /
 // row_scale[m]), zero beyond r (row_scale null: no division), and out [M, r] =
-// RNbf16(S); either may be null.  L % 8 == 0.  dependent: launched beside the
+// RNbf16(S); either may be null.  L % 8 == 0.  after: kBeside, launched beside the
 // kernel before it (launch_mx_quantize), which wrote row_scale and nothing else
-// that is read here.  QLORA_OK or QLORA_ERR_CUDA.
+// that is read here; kWaits, only the set-up is beside it.  QLORA_OK or
+// QLORA_ERR_CUDA.
+enum class After { kEnds, kBeside, kWaits };
 int launch_mx_down(const void* Z, const void* R, bool r_rows, int M, int L, int r, int RP, float s,
-                   const float* row_scale, void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms);
+                   const float* row_scale, void* pad, void* out, After after, int* status, cudaStream_t st, int num_sms);
 
 // dA [r, K] = RNbf16(sU^T Xd), dB [N, r] = RNbf16(s dY^T T) over M tokens; sU has
 // ldu columns.  QLORA_OK or QLORA_ERR_CUDA.

@@ -36,12 +36,6 @@ int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const M
 
 constexpr int kFewTokens = 32;                     // up to here the kernel for few tokens
 
-// Wait for the grid that this one was launched after (returns at once when the
-// launch had no such attribute).
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // True in one lane of a converged warp.  The tensor-core and TMA instructions
 // take their operands from uniform registers; behind an elect.sync the compiler
 // knows that one lane is active and issues them directly, behind a comparison of

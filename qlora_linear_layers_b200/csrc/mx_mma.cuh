@@ -1,16 +1,9 @@
-// Warp-level bf16 tensor-core product for the adapter's small matrices, and the
-// trigger that lets a dependent grid start.
+// Warp-level bf16 tensor-core product for the adapter's small matrices.
 #pragma once
 
 #include <cstdint>
 
 namespace qnf4 {
-
-// The next grid, if it was launched as a dependent, may start once every CTA of
-// this one has passed here; it waits for this grid's end where it needs it.
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {

@@ -260,13 +260,16 @@ k_mx_quantize(const T* __restrict__ X, int64_t ld, int rows, int K, uint8_t* __r
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;   // rows past the last write the padding's zero scales
   quantise_row<T, FMT, KEEP>(X + row * ld, row < rows, row, K, threadIdx.x, blockDim.x, packed, scales, row_scale,
                              status, s_max);
+  // beside the kernel before it, this grid does not end before that one: what waits
+  // for this grid waits for both
+  if (blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 // Threads and rows of a CTA: a unit a thread up to 256 units, several rows a CTA
 // when they are short (a CTA a row: 400000 x 64 bf16 took 419 us).
 template <typename T, int FMT>
 static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int64_t ld, uint8_t* packed,
-                                 uint8_t* scales, float* row_scale, int* status, cudaStream_t s) {
+                                 uint8_t* scales, float* row_scale, bool beside, int* status, cudaStream_t s) {
   constexpr int E = Unit<T>::kElems;
   constexpr int kGroup = 4 * mx_block(FMT) / E;
   const int units = (int)(cols / E);
@@ -280,8 +283,16 @@ static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int6
       while (nt < upad) nt *= 2;
     }
     while (nt <= 32 && group * nt < 256) group *= 2;               // at most 128: divides prow
-    kern<<<(unsigned)(prow / group), dim3(nt, group), 0, s>>>((const T*)X, ld, (int)rows, (int)cols, packed, scales,
-                                                              row_scale, status);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(prow / group), 1, 1);
+    cfg.blockDim = dim3((unsigned)nt, (unsigned)group, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = beside ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, kern, (const T*)X, ld, (int)rows, (int)cols, packed, scales, row_scale, status);
   };
   if (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);
   else if (upad <= 256) run(k_mx_quantize<T, FMT, 1>, 1);
@@ -291,14 +302,14 @@ static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int6
 }
 
 void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
-                        uint8_t* packed, uint8_t* scales, float* row_scale, int* status,
+                        uint8_t* packed, uint8_t* scales, float* row_scale, bool beside, int* status,
                         cudaStream_t s) {
   if (dtype == QLORA_F32) {
-    if (format == QLORA_NVFP4) launch_mx_quantize_t<float, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
-    else launch_mx_quantize_t<float, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+    if (format == QLORA_NVFP4) launch_mx_quantize_t<float, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, beside, status, s);
+    else launch_mx_quantize_t<float, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, beside, status, s);
   } else {
-    if (format == QLORA_NVFP4) launch_mx_quantize_t<__nv_bfloat16, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
-    else launch_mx_quantize_t<__nv_bfloat16, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, status, s);
+    if (format == QLORA_NVFP4) launch_mx_quantize_t<__nv_bfloat16, QLORA_NVFP4>(X, rows, cols, ld, packed, scales, row_scale, beside, status, s);
+    else launch_mx_quantize_t<__nv_bfloat16, QLORA_MXFP4>(X, rows, cols, ld, packed, scales, row_scale, beside, status, s);
   }
 }
 

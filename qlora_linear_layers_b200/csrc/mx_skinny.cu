@@ -57,6 +57,7 @@ struct Args {
   int r, N, RP;             // rank; MMA N (a power of two, 16 to 128); padded width
   int log_splits;
   int ns, b_bytes;          // stages and the bytes of B in one
+  int wait_first;           // read nothing before the kernel before this one has ended
   int* status;
 };
 
@@ -174,6 +175,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     if (elect_one()) {
       int s = 0, i = k0;
       uint32_t ph = 0;
+      if (g.wait_first) grid_dependency_wait();
       for (; i < k1; ++i) {
         if (!mbar_wait(&S.empty[s], ph ^ 1, abort, g.status)) break;
         mbar_arrive_expect_tx(&S.full[s], stage_bytes);
@@ -222,7 +224,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     mbar_wait(&S.acc_full, 0, abort, g.status);
     // as a dependent of the quantisation (whose row scales may be read below) this
     // grid does not end before that one
-    mx::grid_dependency_wait();
+    grid_dependency_wait();
   }
   __syncwarp();
   const int quad = warp & 3;
@@ -310,7 +312,7 @@ static void shape(Args& g, int num_sms) {
 
 template <bool OUTER, bool RT>
 static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
-                  const Args& g, bool dependent, cudaStream_t s) {
+                  const Args& g, bool beside, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_devs{0};
   set_smem_attr_once(k_mx_skinny<OUTER, RT>, 224 * 1024, attr_devs);
   cudaLaunchConfig_t cfg = {};
@@ -326,14 +328,14 @@ static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMa
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
+  cfg.numAttrs = beside ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_mx_skinny<OUTER, RT>, a0, b0, a1, b1, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 }  // namespace skinny
 
 int launch_mx_down(const void* Z, const void* R, bool r_rows, int M, int L, int r, int RP, float s,
-                   const float* row_scale, void* pad, void* out, bool dependent, int* status, cudaStream_t st, int num_sms) {
+                   const float* row_scale, void* pad, void* out, After after, int* status, cudaStream_t st, int num_sms) {
   using namespace skinny;
   Args g{};
   g.L = L;
@@ -343,12 +345,14 @@ int launch_mx_down(const void* Z, const void* R, bool r_rows, int M, int L, int 
   g.status = status;
   g.p[0] = Problem{M, (M + 127) / 128, row_scale, (__nv_bfloat16*)pad, (__nv_bfloat16*)out, 0, s};
   g.b_bytes = r_rows ? (g.N + 63) / 64 * 8192 : g.N * 128;
+  g.wait_first = after == After::kWaits;
   shape(g, num_sms);
   CUtensorMap a, b;
   if (!make_tmap_2d_bf16(&a, Z, L, M, L, 64, 128) ||
       !(r_rows ? make_tmap_2d_bf16(&b, R, r, L, r, 64, 64) : make_tmap_2d_bf16(&b, R, L, r, L, 64, g.N)))
     return QLORA_ERR_CUDA;
-  return r_rows ? launch<false, true>(a, b, a, b, g, dependent, st) : launch<false, false>(a, b, a, b, g, dependent, st);
+  const bool beside = after != After::kEnds;
+  return r_rows ? launch<false, true>(a, b, a, b, g, beside, st) : launch<false, false>(a, b, a, b, g, beside, st);
 }
 
 int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, const void* dY, int N, const void* T,
@@ -378,6 +382,7 @@ int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, co
 __global__ void __launch_bounds__(256)
 k_mx_transpose(const __nv_bfloat16* __restrict__ A, int r, int K, int RP, __nv_bfloat16* __restrict__ At) {
   __shared__ uint16_t tile[64][130];               // [column of A][row of A]
+  grid_launch_dependents();
   const int tid = threadIdx.x, k0 = blockIdx.x * 64;
   for (int i = tid; i < RP * 8; i += 256) {
     const int j = i >> 3, k = 8 * (i & 7);
