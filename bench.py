@@ -68,13 +68,16 @@ def parse():
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-extras", action="store_true",
                     help="skip the per-workload kernel timings after the step")
-    ap.add_argument("--case", choices=["fwd", "bwd", "quantize", "dequantize", "dq", "decode", "merge"],
+    ap.add_argument("--case", choices=["fwd", "bwd", "quantize", "dequantize", "dq", "decode", "merge",
+                                       "mx_quantize", "mx_dequantize", "mx_fwd", "mx_bwd", "dropout"],
                     help="profiling aid: run one operation on one projection and exit")
     ap.add_argument("--proj", type=int, default=0, help="--case: projection 0 gate, 1 up, 2 down")
     ap.add_argument("--workload", default=WORKLOAD,
                     help="--case: workload whose weight shape and rank to use (mlp_7b, decode_70b, "
                          "attn_proj_4096, bwd_4096)")
     ap.add_argument("--tokens", type=int, default=2048, help="--case: token count")
+    ap.add_argument("--format", choices=["mxfp4", "nvfp4"], default="nvfp4", help="--case mx_*: weight format")
+    ap.add_argument("--dropout", type=float, default=0.0, help="--case mx_fwd, mx_bwd, dropout: probability")
     ap.add_argument("--repeat", type=int, default=3, help="--case: timed calls after one warm-up call")
     return ap.parse_args()
 
@@ -804,6 +807,19 @@ def run_case(args):
         "dequantize": lambda: q.nf4_dequantize(wq, Wd),
         "merge": lambda: q.qlora_merge(wq, A, B, alpha, Wd),
     }
+    if args.case.startswith("mx_"):
+        p = args.dropout
+        mx = q.mx_quantize(W, _lib.QLORA_NVFP4 if args.format == "nvfp4" else _lib.QLORA_MXFP4)
+        ws = torch.empty(max(q.workspace_bytes(op, M, N, K, r) for op in
+                             (_lib.QLORA_OP_MX_FWD_DROPOUT, _lib.QLORA_OP_MX_BWD_DROPOUT)),
+                         dtype=torch.uint8, device=dev)
+        ops.update({
+            "mx_quantize": lambda: q.qlora_mx_quantize(W, mx),
+            "mx_dequantize": lambda: q.qlora_mx_dequantize(mx, Wd),
+            "mx_fwd": lambda: q.qlora_mx_linear_fwd(mx, X, A, B, alpha, Y, T, p=p, seed=1, ws=ws),
+            "mx_bwd": lambda: q.qlora_mx_linear_bwd(mx, X, dY, A, B, alpha, dX, dA, dB, T=T, p=p, seed=1, ws=ws),
+        })
+    ops["dropout"] = lambda: q.qlora_dropout_fwd(X, args.dropout, 1, dX)
     torch.cuda.synchronize()
     ops[args.case]()                                  # warm-up call
     torch.cuda.synchronize()
