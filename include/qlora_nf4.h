@@ -430,7 +430,8 @@ int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
  * as for qlora_linear_fwd_dropout; r = 0 with A, B, T_save and dropout NULL is
  * the layer without an adapter.  The adapter runs in the product's own
  * accumulator: with NVFP4 its bf16 factors are divided by the row scales
- * (exact for powers of two).
+ * (exact for powers of two).  The outputs and ws overlap neither an input nor
+ * one another, here and in the backward.
  * Constraints: M >= 1, N % 8 == 0, K % 64 == 0, r in {0, 8, 16, 32, 64, 128},
  * ws of qlora_workspace_bytes(QLORA_OP_MX_FWD, M, N, K, r) bytes, with dropout
  * of QLORA_OP_MX_FWD_DROPOUT.

@@ -100,8 +100,9 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
   const int ls = PAIR ? 0 : g.log_splits, splits = 1 << ls;
   const int half = PAIR ? (int)cluster_ctarank() : 0, rank = PAIR ? 0 : (int)cluster_ctarank();
   const bool leader = half == 0;
-  const int c0 = (int)(blockIdx.x >> ls) * 128;                              // columns of W
-  const int m0 = (int)blockIdx.y * BN, mb = m0 + half * Sh::B_ROWS;          // tokens
+  const unsigned tile = blockIdx.x >> ls, tiles_c = (unsigned)((p.N + 128 * P - 1) / (128 * P) * P);
+  const int c0 = (int)(tile % tiles_c) * 128;                                // columns of W
+  const int m0 = (int)(tile / tiles_c) * BN, mb = m0 + half * Sh::B_ROWS;    // tokens
   const int nk_all = (g.rows + 63) / 64;
   const int k0 = (int)(((int64_t)nk_all * rank) >> ls), k1 = (int)(((int64_t)nk_all * (rank + 1)) >> ls);
   const int na = rank == 0 ? g.na : 0;
@@ -393,7 +394,7 @@ static int launch(const qlora_mx_tensor* w, const void* dY, const void* A, int r
   set_smem_attr_once(k_mx_dx<FMT, BN, PAIR>, (int)bytes, attr_devs);
   cudaLaunchConfig_t cfg = {};
   constexpr int cols = 128 * Sh::kCtas;
-  cfg.gridDim = dim3((unsigned)((K + cols - 1) / cols * Sh::kCtas) << g.log_splits, (unsigned)((M + BN - 1) / BN), 1);
+  cfg.gridDim = dim3((unsigned)((K + cols - 1) / cols * Sh::kCtas) * (unsigned)((M + BN - 1) / BN) << g.log_splits, 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;

@@ -146,7 +146,8 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int splits = 1 << log_splits;
   const int rank = (int)cluster_ctarank();
-  const int n0 = (int)(blockIdx.x >> log_splits) * BW, m0 = blockIdx.y * BN;
+  const unsigned tile = blockIdx.x >> log_splits, tiles_n = (unsigned)(p.N + BW - 1) / BW;
+  const int n0 = (int)(tile % tiles_n) * BW, m0 = (int)(tile / tiles_n) * BN;
   const int nk_all = (p.K + 255) / 256;
   const int k0 = (int)(((int64_t)nk_all * rank) >> log_splits), k1 = (int)(((int64_t)nk_all * (rank + 1)) >> log_splits);
   const int na = !Sh::OWN_PART && rank == 0 ? p.na : 0;
@@ -392,7 +393,7 @@ static int launch(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAd
   int log_splits = 0;
   split_cost(a, BN, num_sms, &log_splits);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.N + BW - 1) / BW) << log_splits, (unsigned)((a.M + BN - 1) / BN), 1);
+  cfg.gridDim = dim3((unsigned)((a.N + BW - 1) / BW) * (unsigned)((a.M + BN - 1) / BN) << log_splits, 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;

@@ -457,7 +457,8 @@ k_mx_dequant_t(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ s
                const float* __restrict__ row_scale, int N, int K, __nv_bfloat16* __restrict__ Wt) {
   constexpr int kPitch = 36;                       // words per transposed row (32 + pad, 16-byte rows)
   __shared__ __align__(16) uint32_t tileT[256 * kPitch];
-  const int n0 = blockIdx.y * 64, k0 = blockIdx.x * 256;
+  const unsigned tiles_k = (unsigned)(K + 255) / 256;
+  const int n0 = (int)(blockIdx.x / tiles_k) * 64, k0 = (int)(blockIdx.x % tiles_k) * 256;
   const int tid = threadIdx.x;
   const int pr = tid & 31, qk = tid >> 5;
   const int k = k0 + 32 * qk;
@@ -505,7 +506,7 @@ k_mx_dequant_t(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ s
 }
 
 void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s) {
-  const dim3 grid((unsigned)((w->cols + 255) / 256), (unsigned)((w->rows + 63) / 64));
+  const unsigned grid = (unsigned)((w->cols + 255) / 256) * (unsigned)((w->rows + 63) / 64);
   auto run = [&](auto kern) {
     kern<<<grid, 256, 0, s>>>(w->packed, w->scales, w->row_scale, (int)w->rows, (int)w->cols, (__nv_bfloat16*)Wt);
   };

@@ -420,7 +420,7 @@ k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restr
   __shared__ __align__(16) float s_ad[8][16][36];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int m0 = (int)blockIdx.y * 128 + warp * 16, k0 = (int)blockIdx.x * 32;
+  const int m0 = (int)(blockIdx.x / (unsigned)(K / 32)) * 128 + warp * 16, k0 = (int)(blockIdx.x % (unsigned)(K / 32)) * 32;
   if (m0 >= M) return;
   float acc[4][4];
 #pragma unroll
@@ -467,7 +467,7 @@ k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restr
 
 void launch_mx_rank_add(const void* sU, const void* At, int RP, int M, int K, void* dX, const Dropout& drop,
                         cudaStream_t s) {
-  const dim3 grid((unsigned)(K / 32), (unsigned)((M + 127) / 128));
+  const unsigned grid = (unsigned)(K / 32) * (unsigned)((M + 127) / 128);
   k_mx_rank_add<<<grid, 256, 0, s>>>((const __nv_bfloat16*)sU, (const __nv_bfloat16*)At, RP, M, K, (__nv_bfloat16*)dX,
                                      make_keys(drop));
 }

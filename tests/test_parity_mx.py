@@ -616,3 +616,26 @@ def test_offsets_past_32_bits(q, fmt):
     x = torch.randn(40000, 64, generator=g, device="cuda")
     Y = q.mx_matmul(q.mx_quantize(x, fmt), w)
     assert torch.equal(Y[-200:], q.mx_matmul(q.mx_quantize(x[-200:].contiguous(), fmt), w))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_more_tiles_of_tokens_than_65535(q, fmt):
+    """The last rows of 65536 tiles of tokens and a piece, against fp64 products of them alone."""
+    M, N, K, r, s, p, seed, n = 65536 * 128 + 5, 8, 64, 8, 2.0, 0.25, 7, 300
+    bf, g = torch.bfloat16, torch.Generator("cuda").manual_seed(1)
+    X, dY = (torch.randn(M, k, generator=g, device="cuda", dtype=bf) for k in (K, N))
+    A, B = (torch.randn(*k, generator=g, device="cuda", dtype=bf) * 0.1 for k in ((r, K), (N, r)))
+    w = q.mx_quantize(torch.randn(N, K, generator=g, device="cuda", dtype=bf), fmt)
+    Y, T = q.mx_linear_fwd(w, X, A, B, s * r, p=p, seed=seed)
+    dX, dA, dB = q.mx_linear_bwd(w, X, dY, A, B, s * r, p=p, seed=seed, T=T)
+    Y0 = q.mx_matmul(q.mx_quantize(X, fmt), w)
+    x, d = X[-n:], dY[-n:].double()
+    xd = q.dropout_fwd(x, p, seed, first=(M - n) * K).double()
+    keep = q.dropout_fwd(torch.ones_like(x), p, seed, first=(M - n) * K) != 0
+    vw, vx, a, b = q.mx_dequantize(w).double(), q.mx_dequantize(q.mx_quantize(x, fmt)).double(), A.double(), B.double()
+    t, u = xd @ a.T, d @ b
+    for got, ref, halves in ((Y0, vx @ vw.T, 1), (Y, vx @ vw.T + s * t @ b.T, 1), (T, t, 1),
+                             (dX, d @ vw + keep * (s / (1 - p)) * (u @ a), 2)):   # dX is rounded twice
+        assert float((got[-n:].double() - ref).norm()) <= halves * H * float(ref.norm())
+    assert torch.isfinite(dA.double()).all() and torch.isfinite(dB.double()).all()
+    assert q.qlora_check_status() == 0
