@@ -5,8 +5,9 @@
 //   forward   Y  = RN(RN32(D c X) + R)      backward   dX = RN(RN32(D c dY))
 //
 // D keeps element e = first + row * cols + col.  Bytes: each input read once,
-// the output written once; the generator costs twenty 64 x 64-bit products a
-// block, which is what bounds bf16 tensors.
+// the output written once; the generator costs 18 64 x 64-bit products a
+// block, which is what bounds bf16 tensors (8192 x 3584: 48 us, with a residual 49
+// us; the bytes alone 18 and 27 us).
 
 #include <algorithm>
 #include <cstdint>
