@@ -168,6 +168,8 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       uint32_t ph = 0, tp = 0;                     // stage, its phase; the tile's phase
       bool ok = true;
       for (int tile = cluster; tile < n_tiles && ok; tile += n_clusters, tp ^= 1) {
+        // where the tokens' scales begin in their 128-row block's four columns: 0 or, with
+        // tiles of 192, 2 (an odd one is a misaligned address)
         const uint32_t sub = (uint32_t)((tile / tiles_n) * PN % 128) / 32;
         ok = mbar_wait_cluster(&S.acc_empty, tp ^ 1, abort, p.status);
         if (!ok) break;
@@ -225,7 +227,7 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
     const uint32_t acc_empty0 = mapa_shared(smem_u32(&S.acc_empty), 0);
     // this lane's row of the four blocks of a stmatrix: token lane % 8, outputs 8 (lane / 8) ..
     const uint32_t row_off = (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
-    uint32_t tp = 0;
+    uint32_t tp = 0, buf = 0;
     bool ok = true;
     grid_dependency_wait();
     for (int tile = cluster; tile < n_tiles; tile += n_clusters, tp ^= 1) {
@@ -292,7 +294,8 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             }
           }
         }
-        uint8_t* out = S.out[e][c & 1];
+        uint8_t* out = S.out[e][buf];
+        buf ^= 1;                                  // across tiles too: one of 192 tokens has three chunks
         if (lane == 0) store_wait_read<1>();       // the store before the last one has left its chunk
         __syncwarp();
         const uint32_t to = smem_u32(out) + row_off;

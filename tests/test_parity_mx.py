@@ -199,6 +199,31 @@ def test_product(q, fmt, M, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K,r", [(4096, 4096, 512, 8), (4000, 4090, 544, 0), (2040, 2568, 576, 64), (2220, 2560, 256, 0),
+                                     (8100, 600, 2048, 128)])
+def test_product_in_rounds_of_tiles(q, fmt, M, N, K, r):
+    """More tiles than pairs of SMs, the last round in halves or not, on the GPU in fp64."""
+    g = torch.Generator("cuda").manual_seed(M)
+    x = q.mx_quantize(torch.randn(M, K, generator=g, device="cuda"), fmt)
+    w = q.mx_quantize(torch.randn(N, K, generator=g, device="cuda"), fmt)
+    vx, vw = q.mx_dequantize(x).double(), q.mx_dequantize(w).double()
+    ref, mag = vx @ vw.T, vx.abs() @ vw.abs().T
+    err = (q.mx_matmul(x, w).double() - ref).abs()
+    assert float((err - H * ref.abs() - (1 + H) * (K + 2) * U * mag).max()) <= 0
+    if r:
+        X = q.mx_dequantize(x)                     # X quantised again is X
+        A, B = (torch.randn(*k, generator=g, device="cuda").bfloat16() for k in ((r, K), (N, r)))
+        Y, T = q.mx_linear_fwd(w, X, A, B, float(r))
+        t = vx @ A.double().T
+        b, ref = B.double().abs(), ref + t @ B.double().T
+        t_mag = vx.abs() @ A.double().abs().T      # T: its sum, and its rounding
+        ad = (H * t.abs() + (1 + H) * K * U * t_mag) @ b.T
+        bound = H * ref.abs() + (1 + H) * (ad + (K + r + 2) * U * (mag + (1 + H) * t_mag @ b.T))
+        assert float(((Y.double() - ref).abs() - bound).max()) <= 0
+    assert q.qlora_check_status() == 0
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 def test_product_reads_out_the_weight(q, fmt):
     """One-hot rows of x return columns of the stored weight, rounded once (an
     NVFP4 block of a single 1 stores 6 * E4M3(2^11 / 6) * 2^-11 = 1.03125)."""
