@@ -250,6 +250,7 @@ def qlora_linear_bwd_dropout(w: NF4Tensor, X, dY, A, B, alpha: float, p: float, 
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice      # without the initialisation that a CUDA tensor implies
 
 
 class _On:
@@ -265,7 +266,7 @@ class _On:
             if self.stream.device.index != self.dev:
                 raise ValueError("the stream is on another device than the tensors")
             self.ctx = torch.cuda.stream(self.stream)
-        elif self.dev != torch.cuda.current_device():
+        elif self.dev != _current_device():
             self.ctx = torch.cuda.device(self.dev)
         if self.ctx is not None:
             self.ctx.__enter__()
