@@ -298,7 +298,7 @@ static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int6
     cfg.numAttrs = beside ? 1 : 0;
     cudaLaunchKernelEx(&cfg, kern, (const T*)X, ld, (int)rows, (int)cols, packed, scales, row_scale, status);
   };
-  if (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);
+  if constexpr (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);
   else if (upad <= 256) run(k_mx_quantize<T, FMT, 1>, 1);
   else if (upad <= 1024) run(k_mx_quantize<T, FMT, 2>, 2);
   else if (upad <= 1536) run(k_mx_quantize<T, FMT, 3>, 3);
