@@ -864,7 +864,7 @@ int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY,
   take_gemm_events(&e0, &e1);
   if (inside) {
     if (e0) cudaEventRecord(e0, s);
-    st = launch_mx_dx(w, dY, (int)M, A, r, sU, RP, na, dX, d->status, s, d->sms);
+    st = launch_mx_dx(w, dY, (int)M, A, r, sU, RP, na, dX, r != 0, d->status, s, d->sms);
   } else {
     launch_mx_dequant_t(w, Wt, s);
     ++n;

@@ -86,7 +86,8 @@ int launch_mx_down(const void* Z, const void* R, bool r_rows, int M, int L, int 
                    const float* row_scale, void* pad, void* out, After after, int* status, cudaStream_t st, int num_sms);
 
 // dA [r, K] = RNbf16(sU^T Xd), dB [N, r] = RNbf16(s dY^T T) over M tokens; sU has
-// ldu columns.  QLORA_OK or QLORA_ERR_CUDA.
+// ldu columns.  Only its set-up is beside the kernel before it.  QLORA_OK or
+// QLORA_ERR_CUDA.
 int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, const void* dY, int N, const void* T,
                     float s, void* dB, int M, int r, int* status, cudaStream_t st, int num_sms);
 
@@ -95,9 +96,10 @@ void launch_mx_transpose(const void* A, int r, int K, int RP, void* At, cudaStre
 
 // dX [M, K] = dY deq(W) + sU A over RP = 64 na columns of sU [M, RP] (na = 0: the
 // first term alone), W expanded inside the product; mx_dx_expands_inside: whether
-// that is the faster way for these sizes.  QLORA_OK or QLORA_ERR_CUDA.
+// that is the faster way for these sizes.  beside: launched as the dependent of the
+// kernel before it, of whose results it reads sU alone.  QLORA_OK or QLORA_ERR_CUDA.
 bool mx_dx_expands_inside(int M, int N, int K, int na, int num_sms);
 int launch_mx_dx(const qlora_mx_tensor* w, const void* dY, int M, const void* A, int r, const void* sU, int RP, int na,
-                 void* dX, int* status, cudaStream_t s, int num_sms);
+                 void* dX, bool beside, int* status, cudaStream_t s, int num_sms);
 
 }  // namespace qnf4

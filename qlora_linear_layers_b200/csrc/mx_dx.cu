@@ -94,6 +94,7 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
   constexpr int NS = Sh::NS, P = Sh::kCtas;
   static_assert(BN * 512 <= NS * (A_BYTES + Sh::B_BYTES), "reduction buffer");
   extern __shared__ uint8_t smem_raw[];
+  grid_launch_dependents();
   Smem<BN, PAIR>& S = *smem_align1024<Smem<BN, PAIR>>(smem_raw);
   const Args& p = g.out;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -152,6 +153,7 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
     if (elect_one()) {
       int s = 0, i = -na;
       uint32_t ph = 0;
+      if (na) grid_dependency_wait();              // sU comes from the kernel before
       for (; i < k1 - k0; ++i) {
         if (!wait(&S.empty[s], ph ^ 1)) break;
         if (i < 0) {
@@ -255,6 +257,7 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
       }
     }
   } else {
+    grid_dependency_wait();                        // this grid does not end before that kernel
     wait(&S.acc_full, 0);
   }
   __syncwarp();
@@ -378,7 +381,7 @@ static int64_t cost_expanded(int M, int N, int K, int na, int num_sms) {
 
 template <int FMT, int BN, bool PAIR>
 static int launch(const qlora_mx_tensor* w, const void* dY, const void* A, int r, const void* sU, int RP, DxArgs g,
-                  cudaStream_t s) {
+                  bool beside, cudaStream_t s) {
   using Sh = Shape<BN, PAIR>;
   CUtensorMap ty, ta, tu, to;
   const int M = g.out.M, K = g.out.N;
@@ -398,29 +401,31 @@ static int launch(const qlora_mx_tensor* w, const void* dY, const void* A, int r
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)Sh::kCtas << g.log_splits;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k_mx_dx<FMT, BN, PAIR>, ty, ta, tu, to, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
 template <int FMT>
 static int launch_fmt(const qlora_mx_tensor* w, const void* dY, const void* A, int r, const void* sU, int RP, DxArgs g,
-                      cudaStream_t s, int num_sms) {
+                      bool beside, cudaStream_t s, int num_sms) {
   int bn = 0;
   bool pair = false;
   cost(g.out.M, g.rows, g.out.N, g.na, num_sms, &bn, &pair, &g.log_splits);
-  if (pair) return launch<FMT, 256, true>(w, dY, A, r, sU, RP, g, s);
+  if (pair) return launch<FMT, 256, true>(w, dY, A, r, sU, RP, g, beside, s);
   switch (bn) {
-    case 16: return launch<FMT, 16, false>(w, dY, A, r, sU, RP, g, s);
-    case 32: return launch<FMT, 32, false>(w, dY, A, r, sU, RP, g, s);
-    case 64: return launch<FMT, 64, false>(w, dY, A, r, sU, RP, g, s);
-    case 128: return launch<FMT, 128, false>(w, dY, A, r, sU, RP, g, s);
-    default: return launch<FMT, 256, false>(w, dY, A, r, sU, RP, g, s);
+    case 16: return launch<FMT, 16, false>(w, dY, A, r, sU, RP, g, beside, s);
+    case 32: return launch<FMT, 32, false>(w, dY, A, r, sU, RP, g, beside, s);
+    case 64: return launch<FMT, 64, false>(w, dY, A, r, sU, RP, g, beside, s);
+    case 128: return launch<FMT, 128, false>(w, dY, A, r, sU, RP, g, beside, s);
+    default: return launch<FMT, 256, false>(w, dY, A, r, sU, RP, g, beside, s);
   }
 }
 
@@ -433,7 +438,7 @@ bool mx_dx_expands_inside(int M, int N, int K, int na, int num_sms) {
 }
 
 int launch_mx_dx(const qlora_mx_tensor* w, const void* dY, int M, const void* A, int r, const void* sU, int RP, int na,
-                 void* dX, int* status, cudaStream_t s, int num_sms) {
+                 void* dX, bool beside, int* status, cudaStream_t s, int num_sms) {
   dx::DxArgs g{};
   g.out.out = static_cast<__nv_bfloat16*>(dX);
   g.out.M = M;
@@ -444,8 +449,8 @@ int launch_mx_dx(const qlora_mx_tensor* w, const void* dY, int M, const void* A,
   g.rows = (int)w->rows;
   g.na = na;
   g.status = status;
-  return w->format == QLORA_NVFP4 ? dx::launch_fmt<QLORA_NVFP4>(w, dY, A, r, sU, RP, g, s, num_sms)
-                                  : dx::launch_fmt<QLORA_MXFP4>(w, dY, A, r, sU, RP, g, s, num_sms);
+  return w->format == QLORA_NVFP4 ? dx::launch_fmt<QLORA_NVFP4>(w, dY, A, r, sU, RP, g, beside, s, num_sms)
+                                  : dx::launch_fmt<QLORA_MXFP4>(w, dY, A, r, sU, RP, g, beside, s, num_sms);
 }
 
 }  // namespace qnf4

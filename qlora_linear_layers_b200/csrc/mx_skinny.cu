@@ -369,12 +369,13 @@ int launch_mx_outer(const void* Xd, int K, const void* sU, int ldu, void* dA, co
   g.p[0] = Problem{K, (K + 127) / 128, nullptr, nullptr, (__nv_bfloat16*)dA, 1, 1.0f};
   g.p[1] = Problem{N, (N + 127) / 128, nullptr, nullptr, (__nv_bfloat16*)dB, 0, s};
   g.b_bytes = (g.N + 63) / 64 * 8192;
+  g.wait_first = 1;
   shape(g, num_sms);
   CUtensorMap a0, b0, a1, b1;
   if (!make_tmap_2d_bf16(&a0, Xd, K, M, K, 64, 64) || !make_tmap_2d_bf16(&b0, sU, r, M, ldu, 64, 64) ||
       !make_tmap_2d_bf16(&a1, dY, N, M, N, 64, 64) || !make_tmap_2d_bf16(&b1, T, r, M, r, 64, 64))
     return QLORA_ERR_CUDA;
-  return launch<true, false>(a0, b0, a1, b1, g, false, st);
+  return launch<true, false>(a0, b0, a1, b1, g, true, st);
 }
 
 // ===========================================================================
