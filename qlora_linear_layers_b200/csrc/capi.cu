@@ -788,10 +788,10 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
       quantise(true);
       st = down(wsb + lay.xd, After::kWaits);
     } else if (div) {
-      quantise(false);
+      quantise(n > 2);                             // beside the factor that reads B
       st = down(X, After::kBeside);
     } else {
-      st = down(X, After::kEnds);
+      st = down(X, n > 2 ? After::kBeside : After::kEnds);
       if (!st) quantise(true);
     }
     if (st) return st;
@@ -866,7 +866,7 @@ int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY,
     if (e0) cudaEventRecord(e0, s);
     st = launch_mx_dx(w, dY, (int)M, A, r, sU, RP, na, dX, r != 0, d->status, s, d->sms);
   } else {
-    launch_mx_dequant_t(w, Wt, s);
+    launch_mx_dequant_t(w, Wt, r != 0, s);
     ++n;
     // dX[M, K] = dY Wt^T + sU At^T
     GemmArgs a{};

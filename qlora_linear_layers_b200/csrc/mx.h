@@ -22,13 +22,30 @@ __host__ __device__ constexpr int64_t mx_scale_offset(int64_t r, int64_t c, int6
   return ((r >> 7) * tiles + (c >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (c & 3);
 }
 
-// beside: launched beside the kernel before it, of which it reads nothing, and
-// ending after it.
+// A launch that may begin when every CTA of the kernel before it has called
+// grid_launch_dependents or ended.
+template <typename... P, typename... A>
+void launch_dependent(void (*kern)(P...), dim3 grid, dim3 block, bool dependent, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+// beside (here and below): launched beside the kernel before it, of which it reads
+// nothing, and ending after it.
 void launch_mx_quantize(const void* X, int dtype, int64_t rows, int64_t cols, int64_t ld, int format,
                         uint8_t* packed, uint8_t* scales, float* row_scale, bool beside, int* status,
                         cudaStream_t s);
 struct Dropout;
 // dX [M, K] (bf16, in place) += D c (sU [M, RP] At [K, RP]^T), K % 64 == 0.
+// It reads nothing before the kernel before it has ended.
 void launch_mx_rank_add(const void* sU, const void* At, int RP, int M, int K, void* dX, const Dropout& drop,
                         cudaStream_t s);
 
@@ -43,7 +60,7 @@ void launch_mx_prep(const void* X, int M, int K, const void* A, int r, int forma
 void launch_mx_dequantize(const qlora_mx_tensor* t, void* out, cudaStream_t s);
 
 // Wt[cols, rows] = deq(W)^T, bf16 (the values of qlora_mx_dequantize).
-void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s);
+void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, bool beside, cudaStream_t s);
 
 // out[rows, RP] = RNbf16(in[rows, :r] / row_scale[row]), zero beyond r; no
 // division when row_scale is null.  `in` has ldi elements a row; out may be in.

@@ -287,16 +287,8 @@ static void launch_mx_quantize_t(const void* X, int64_t rows, int64_t cols, int6
       while (nt < upad) nt *= 2;
     }
     while (nt <= 32 && group * nt < 256) group *= 2;               // at most 128: divides prow
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(prow / group), 1, 1);
-    cfg.blockDim = dim3((unsigned)nt, (unsigned)group, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = beside ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, kern, (const T*)X, ld, (int)rows, (int)cols, packed, scales, row_scale, status);
+    launch_dependent(kern, dim3((unsigned)(prow / group)), dim3(nt, group), beside, s, (const T*)X, ld, (int)rows, (int)cols,
+                     packed, scales, row_scale, status);
   };
   if constexpr (FMT != QLORA_NVFP4) run(k_mx_quantize<T, FMT, 0>, 1);
   else if (upad <= 256) run(k_mx_quantize<T, FMT, 1>, 1);
@@ -508,12 +500,14 @@ k_mx_dequant_t(const uint8_t* __restrict__ packed, const uint8_t* __restrict__ s
       *reinterpret_cast<uint4*>(Wt + (int64_t)kk * N + nn) =
           *reinterpret_cast<const uint4*>(&tileT[kr * kPitch + ch * 4]);
   }
+  if (blockIdx.x == gridDim.x - 1) grid_dependency_wait();         // ends after the kernel it runs beside
 }
 
-void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s) {
+void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, bool beside, cudaStream_t s) {
   const unsigned grid = (unsigned)((w->cols + 255) / 256) * (unsigned)((w->rows + 63) / 64);
   auto run = [&](auto kern) {
-    kern<<<grid, 256, 0, s>>>(w->packed, w->scales, w->row_scale, (int)w->rows, (int)w->cols, (__nv_bfloat16*)Wt);
+    launch_dependent(kern, dim3(grid), dim3(256), beside, s, w->packed, w->scales, w->row_scale, (int)w->rows, (int)w->cols,
+                     (__nv_bfloat16*)Wt);
   };
   if (w->format == QLORA_NVFP4) run(k_mx_dequant_t<QLORA_NVFP4>);
   else run(k_mx_dequant_t<QLORA_MXFP4>);
@@ -528,6 +522,7 @@ void launch_mx_dequant_t(const qlora_mx_tensor* w, void* Wt, cudaStream_t s) {
 __global__ void __launch_bounds__(256)
 k_mx_pad_rows(const __nv_bfloat16* in, int64_t rows, int r, int ldi, int RP, const float* __restrict__ row_scale,
               __nv_bfloat16* out) {
+  grid_launch_dependents();
   const int per = RP / 8;                          // 16-byte words of an output row (8 or 16)
   const int64_t total = rows * per;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;

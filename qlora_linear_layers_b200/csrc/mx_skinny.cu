@@ -427,7 +427,9 @@ k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int m0 = (int)(blockIdx.x / (unsigned)(K / 32)) * 128 + warp * 16, k0 = (int)(blockIdx.x % (unsigned)(K / 32)) * 32;
+  grid_launch_dependents();
   if (m0 >= M) return;
+  grid_dependency_wait();
   float acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.0f;
@@ -474,8 +476,8 @@ k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restr
 void launch_mx_rank_add(const void* sU, const void* At, int RP, int M, int K, void* dX, const Dropout& drop,
                         cudaStream_t s) {
   const unsigned grid = (unsigned)(K / 32) * (unsigned)((M + 127) / 128);
-  k_mx_rank_add<<<grid, 256, 0, s>>>((const __nv_bfloat16*)sU, (const __nv_bfloat16*)At, RP, M, K, (__nv_bfloat16*)dX,
-                                     make_keys(drop));
+  launch_dependent(k_mx_rank_add, dim3(grid), dim3(256), true, s, (const __nv_bfloat16*)sU, (const __nv_bfloat16*)At, RP, M, K,
+                   (__nv_bfloat16*)dX, make_keys(drop));
 }
 
 }  // namespace qnf4
