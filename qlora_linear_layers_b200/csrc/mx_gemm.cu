@@ -226,6 +226,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
+      grid_dependency_wait();                      // the bounded waits begin with the work
       for (int i = -na; i < k1 - k0; ++i) {
         ok = mbar_wait(&S.full[s], ph, abort, p.status);
         if (!ok) break;

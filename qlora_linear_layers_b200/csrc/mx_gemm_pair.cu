@@ -168,6 +168,7 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
       int s = 0;
       uint32_t ph = 0, tp = 0;                     // stage, its phase; the tile's phase
       bool ok = true;
+      grid_dependency_wait();                      // the bounded waits begin with the work
       for (int tile = cluster; tile < n_tiles && ok; tile += n_clusters, tp ^= 1) {
         // where the tokens' scales begin in their 128-row block's four columns: 0 or, with
         // tiles of 192, 2 (an odd one is a misaligned address)

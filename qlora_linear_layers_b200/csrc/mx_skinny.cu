@@ -173,12 +173,12 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   volatile int* abort = &S.abort;
+  if (g.wait_first) grid_dependency_wait();        // in every warp: a bounded wait begins with the work
 
   if (warp == 0) {
     if (elect_one()) {
       int s = 0, i = k0;
       uint32_t ph = 0;
-      if (g.wait_first) grid_dependency_wait();
       for (; i < k1; ++i) {
         if (!mbar_wait(&S.empty[s], ph ^ 1, abort, g.status)) break;
         mbar_arrive_expect_tx(&S.full[s], stage_bytes);
