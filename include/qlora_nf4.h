@@ -169,8 +169,8 @@ typedef enum { QLORA_MXFP4 = 0, QLORA_NVFP4 = 1 } qlora_mx_format;
  *             (r % 128 / 32) * 4 + c % 4, C = cols / block; bytes of rows and
  *             columns past the matrix are 0
  *   row_scale [rows] fp32 (NVFP4; unused for MXFP4).  The quantiser writes
- *             powers of two; any finite positive values are accepted (one
- *             scale for the whole tensor is that scale repeated)
+ *             powers of two, 2^-100 to 2^117; any positive normal values are
+ *             accepted (one scale for the whole tensor is that scale repeated)
  * Value of an element: e2m1(code) * scale (MXFP4), RN32(e2m1(code) * S * s)
  * (NVFP4).  cols % 32 == 0.
  */
@@ -429,9 +429,12 @@ int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
  * s = alpha / r, X' = X, or dropout(X) when `dropout` is not NULL.  Arguments
  * as for qlora_linear_fwd_dropout; r = 0 with A, B, T_save and dropout NULL is
  * the layer without an adapter.  The adapter runs in the product's own
- * accumulator: with NVFP4 its bf16 factors are divided by the row scales
- * (exact for powers of two).  The outputs and ws overlap neither an input nor
- * one another, here and in the backward.
+ * accumulator, or is added after it, as the sizes decide: in the accumulator,
+ * with NVFP4, its bf16 factors s T and B are divided by the row scales of X and
+ * of W (exact for powers of two).  It has to be finite so divided: with the scales
+ * s_n of W that the quantiser writes it is while s 2688 sum |A| |B| < 2^128 s_n
+ * for every row n (2^28 for the smallest scale).  The outputs and ws overlap
+ * neither an input nor one another, here and in the backward.
  * Constraints: M >= 1, N % 8 == 0, K % 64 == 0, r in {0, 8, 16, 32, 64, 128},
  * ws of qlora_workspace_bytes(QLORA_OP_MX_FWD, M, N, K, r) bytes, with dropout
  * of QLORA_OP_MX_FWD_DROPOUT.

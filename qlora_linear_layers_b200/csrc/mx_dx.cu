@@ -330,10 +330,10 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
       const int first = m0 + rank * cs, n_cols = min(cs, p.M - first);
       if (cs >= 8)
         for (int c = 0; c < n_cols; c += 8)
-          add_ranks<8, false>(p, mine + c * 128, cs * 128, splits, first + c, n, 1.0f, nullptr, 0, odd, true);
+          add_ranks<8, false>(p, mine + c * 128, cs * 128, splits, first + c, n, 1.0f, false, nullptr, 0, odd, true);
       else
         for (int c = 0; c < n_cols; c += 2)
-          add_ranks<2, false>(p, mine + c * 128, cs * 128, splits, first + c, n, 1.0f, nullptr, 0, odd, true);
+          add_ranks<2, false>(p, mine + c * 128, cs * 128, splits, first + c, n, 1.0f, false, nullptr, 0, odd, true);
     }
   }
   tc_fence_before();

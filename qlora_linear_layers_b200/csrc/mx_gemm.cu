@@ -183,6 +183,9 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   const int quad = warp & 3;
   const int n = n0 + quad * 32 + lane;             // an epilogue lane's weight row
   const int cs = BN >> log_splits;                 // token columns each rank adds up and stores (even)
+  const int live = min(BN, p.M - m0);              // token columns that exist
+  float rw = 1.0f;
+  bool far = false;                                // a scale of the warp's rows and the tokens is (times_scales)
   if (warp == 0) {
     if (elect_one()) {
       int s = 0, i = -na;
@@ -266,6 +269,12 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
     }
   } else {
     grid_dependency_wait();
+    if (NV) {
+      if (n < p.N) rw = p.wr[n];
+      far = scale_far(rw);
+      for (int c = lane; c < live; c += 32) far |= scale_far(p.xr[m0 + c]);
+      far = __any_sync(0xFFFFFFFFu, far);
+    }
     if constexpr (Sh::OWN_PART) {                  // the adapter, while the MMAs run
       const int row = n0 + quad * 32;
       if (p.r && row < p.N)
@@ -282,12 +291,9 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const bool odd = lane & 1;
   const bool pairs = (p.N & 1) == 0;
-  const int live = min(BN, p.M - m0);              // token columns that exist
   float* part = Sh::OWN_PART ? S.part : reinterpret_cast<float*>(S.w[0]);   // [splits][cs][128]
   if (warp >= 2) {
     tc_fence_after();
-    float rw = 1.0f;
-    if (NV && n < p.N) rw = p.wr[n];
     if (splits == 1) {
 #pragma unroll 1
       for (int c = 0; c < live; c += 16) {
@@ -298,7 +304,7 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float rx = c + j < live ? p.xr[m0 + c + j] : 0.0f;
-            v[j] = __float_as_uint(__fmul_rn(__uint_as_float(v[j]), __fmul_rn(rx, rw)));
+            v[j] = __float_as_uint(times_scales(__uint_as_float(v[j]), rx, rw, far));
           }
         }
         if (Sh::OWN_PART && p.r) {
@@ -327,18 +333,16 @@ k_mx_gemm(const __grid_constant__ CUtensorMap tm_w,       // [N, K / 2] bytes
   if (splits > 1) {
     cluster_sync();                                // the partial sums have arrived
     if (warp >= 2) {
-      float rw = 1.0f;
-      if (NV && n < p.N) rw = p.wr[n];
       const float* mine = part + quad * 32 + lane;
       const int first = m0 + rank * cs, n_cols = min(cs, p.M - first);
       const float* add = Sh::OWN_PART && p.r ? S.add + rank * cs * Sh::ADD_PITCH + quad * 32 + lane : nullptr;
       if (cs >= 8)
         for (int c = 0; c < n_cols; c += 8)
-          add_ranks<8, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, add ? add + c * Sh::ADD_PITCH : nullptr,
+          add_ranks<8, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, far, add ? add + c * Sh::ADD_PITCH : nullptr,
                            Sh::ADD_PITCH, odd, pairs);
       else
         for (int c = 0; c < n_cols; c += 2)
-          add_ranks<2, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, add ? add + c * Sh::ADD_PITCH : nullptr,
+          add_ranks<2, NV>(p, mine + c * 128, cs * 128, splits, first + c, n, rw, far, add ? add + c * Sh::ADD_PITCH : nullptr,
                            Sh::ADD_PITCH, odd, pairs);
     }
   }

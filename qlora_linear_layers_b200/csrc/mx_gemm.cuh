@@ -42,6 +42,19 @@ int launch_gemm_pair(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const M
 
 constexpr int kFewTokens = 32;                     // up to here the kernel for few tokens
 
+// Barrier of `Threads` threads; true if any of them came with true.
+template <int Id, int Threads>
+__device__ __forceinline__ bool barrier_or(bool v) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any) : "r"((uint32_t)v), "n"(Id), "n"(Threads) : "memory");
+  return any != 0;
+}
+
 // True in one lane of a converged warp.  The tensor-core and TMA instructions
 // take their operands from uniform registers; behind an elect.sync the compiler
 // knows that one lane is active and issues them directly, behind a comparison of
@@ -172,6 +185,18 @@ __device__ __forceinline__ void store_wait_read() {
 }
 
 
+// A sum times its two row scales.  Their product is formed first, one multiplication
+// for both and exact for powers of two, where it is a normal number; scales far from 1
+// (`far`) may have a product that is not, although the result is: then the larger one
+// comes first, so that the sum is moved out of range only if the result is.
+__device__ __forceinline__ bool scale_far(float s) { return !(s >= 0x1p-62f && s <= 0x1p62f); }
+__device__ __forceinline__ float times_scales(float x, float rx, float rw, bool far) {
+  const float s = __fmul_rn(rx, rw);
+  if (far && !(s >= 0x1p-126f && s <= 0x1.fffffep127f))
+    return rx > rw ? __fmul_rn(__fmul_rn(x, rx), rw) : __fmul_rn(__fmul_rn(x, rw), rx);
+  return __fmul_rn(x, s);
+}
+
 // Store into another CTA of the cluster (address from mapa_shared).
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(addr), "f"(v) : "memory");
@@ -213,7 +238,7 @@ __device__ __forceinline__ void store_columns(const Args& p, const uint32_t* v, 
 // Add the ranks' partial sums of NC token columns (in rank order), scale, store.
 template <int NC, bool NV>
 __device__ __forceinline__ void add_ranks(const Args& p, const float* part, int rank_stride, int splits, int m, int n,
-                                          float rw, const float* add, int add_pitch, bool odd, bool pairs) {
+                                          float rw, bool far, const float* add, int add_pitch, bool odd, bool pairs) {
   float sum[NC], rx[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) rx[j] = NV && m + j < p.M ? p.xr[m + j] : 0.0f;
@@ -225,7 +250,7 @@ __device__ __forceinline__ void add_ranks(const Args& p, const float* part, int 
   uint32_t v[NC];
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    if (NV) sum[j] = __fmul_rn(sum[j], __fmul_rn(rx[j], rw));
+    if (NV) sum[j] = times_scales(sum[j], rx[j], rw, far);
     if (add) sum[j] = __fadd_rn(sum[j], add[j * add_pitch]);
     v[j] = __float_as_uint(sum[j]);
   }
