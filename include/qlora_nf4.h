@@ -417,7 +417,8 @@ int qlora_mx_dequantize(const qlora_mx_tensor* t, void* out, qlora_stream_t stre
  * Product of two microscaled matrices of one format:
  *   Y[M, N] = RNbf16( deq(x) deq(w)^T ),  x [M, K], w [N, K]
  * on the block-scaled tensor cores (the scales are applied inside the product,
- * sums in fp32), any M, N >= 1, no workspace.  A row's result does not depend
+ * sums in fp32, truncated at each of K / 64 steps: at most 2^-23 of the sum of
+ * magnitudes a step), any M, N >= 1, no workspace.  A row's result does not depend
  * on the other rows of x.  The order of the sum depends on the shapes alone.
  */
 int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y, qlora_stream_t stream);
@@ -449,7 +450,9 @@ int qlora_mx_linear_fwd(const qlora_mx_tensor* w, const void* X, int64_t M, cons
  * with the bf16 values of qlora_mx_dequantize for deq(W); arguments as for
  * qlora_linear_bwd_dropout, `dropout` may be NULL, r = 0 (A, B, T, dA, dB and
  * dropout NULL) computes dX alone.  T is the forward's T_save, or NULL to
- * recompute it.  ws of qlora_workspace_bytes(QLORA_OP_MX_BWD, M, N, K, r) bytes,
+ * recompute it.  dA and dB hold for any M: their sums lose at most 2^-12 of
+ * themselves to the tensor core's truncation (dX: N / 16 steps, see
+ * qlora_mx_matmul).  ws of qlora_workspace_bytes(QLORA_OP_MX_BWD, M, N, K, r) bytes,
  * with dropout of QLORA_OP_MX_BWD_DROPOUT.
  */
 int qlora_mx_linear_bwd(const qlora_mx_tensor* w, const void* X, const void* dY, int64_t M,

@@ -4,7 +4,7 @@
 // for columns while its cluster's other CTAs hold theirs must not wait for one that
 // waits for it.  None has to wait: any kernels of this library that fit an SM
 // together by their shared memory need at most 512 columns together (a product's
-// two CTAs 256 each, the adapter's 128 each; the paired kernels leave no room).
+// two CTAs 256 each, the adapter's 128 or 256 each; the paired kernels leave no room).
 #pragma once
 
 #include <cstdint>

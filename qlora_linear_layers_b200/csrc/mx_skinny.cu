@@ -20,6 +20,12 @@
 //    with three stages a CTA took 0.33 us a stage, 54 GB/s;
 //  * warp 1: tcgen05.mma kind::f16, M = 128, N = r (at least 16);
 //  * warps 2-5: cluster reduction, rounding, stores.
+//
+// The tensor core truncates the sum that it adds to, so a contraction of n MMAs
+// loses up to n half steps of it where all terms have one sign (8.4 M tokens: 65536 MMAs,
+// dA and dB 0.5 % too small, more than their rounding).  A CTA's contraction is cut in
+// runs of kRun stages (2048 MMAs, 2^-12 at most); warps 2-5 add up the runs, rounding
+// to nearest, in columns of their own.
 // Every wait is bounded (QLORA_ERR_TIMEOUT).
 
 #include <algorithm>
@@ -42,6 +48,7 @@ using mx::elect_one;
 
 constexpr int NUM_THREADS = 192;
 constexpr int kMaxStages = 10;
+constexpr int kRun = 512;                          // stages of a run, a power of two
 constexpr int A_BYTES = 128 * 64 * 2;
 
 // One product of a launch (an outer launch has up to two).
@@ -60,6 +67,7 @@ struct Args {
   int r, N, RP;             // rank; MMA N (a power of two, 16 to 128); padded width
   int log_splits;
   int ns, b_bytes;          // stages and the bytes of B in one
+  int cols;                 // tensor-memory columns: 128, or 256 with several runs
   int wait_first;           // read nothing before the kernel before this one has ended
   int* status;
 };
@@ -67,7 +75,7 @@ struct Args {
 // Shared memory: this, then ns stages of A and B, 1024-byte aligned; the
 // reduction's partial sums (N * 512 bytes) take the stages' place.
 struct Head {
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full, acc_empty;
   uint32_t tmem_base;
   int abort;
 };
@@ -157,11 +165,12 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
       mbar_init(&S.empty[i], 1);
     }
     mbar_init(&S.acc_full, 1);
+    mbar_init(&S.acc_empty, 4);
     S.abort = 0;
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&S.tmem_base, 128);
+    tmem_alloc(&S.tmem_base, g.cols);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -173,6 +182,22 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   volatile int* abort = &S.abort;
+  const int runs = (k1 - k0 + kRun - 1) / kRun;
+  const int quad = warp & 3;
+  const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16);
+  // 16 columns of the accumulator, with the runs before it
+  auto sums16 = [&](int c, bool more, float* v) {
+    tmem_ld16(taddr + c, reinterpret_cast<uint32_t*>(v));
+    if (more) {
+      float w[16];
+      tmem_ld16(taddr + 128 + c, reinterpret_cast<uint32_t*>(w));
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = __fadd_rn(v[j], w[j]);
+    } else {
+      tmem_wait_ld();
+    }
+  };
   if (g.wait_first) grid_dependency_wait();        // in every warp: a bounded wait begins with the work
 
   if (warp == 0) {
@@ -207,6 +232,11 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
       int s = 0;
       uint32_t ph = 0;
       for (int i = k0; i < k1; ++i) {
+        const int at = (i - k0) & (kRun - 1);      // stage of the run
+        if (at == 0 && i > k0) {
+          mma_commit(&S.acc_full);
+          if (!mbar_wait(&S.acc_empty, ((i - k0) / kRun - 1) & 1, abort, g.status)) break;
+        }
         if (!mbar_wait(&S.full[s], ph, abort, g.status)) break;
         tc_fence_after();
         const uint32_t aa = smem_u32(stages + s * stage_bytes), bb = aa + A_BYTES;
@@ -216,31 +246,42 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           mma_ss(tmem, a + (OUTER ? kRows : kElems) * q, b + (OUTER || RT ? kRows : kElems) * q, idesc,
-                 (i > k0 || q > 0) ? 1u : 0u);
+                 (at > 0 || q > 0) ? 1u : 0u);
         mma_commit(&S.empty[s]);
         if (++s == NS) { s = 0; ph ^= 1; }
       }
       mma_commit(&S.acc_full);
-      mbar_wait(&S.acc_full, 0, abort, g.status);
+      mbar_wait(&S.acc_full, (runs - 1) & 1, abort, g.status);
     }
   } else {
-    mbar_wait(&S.acc_full, 0, abort, g.status);
+    for (int j = 0; j + 1 < runs && mbar_wait(&S.acc_full, j & 1, abort, g.status); ++j) {
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < g.N; c += 16) {
+        float v[16];
+        sums16(c, j > 0, v);
+        tmem_st16(taddr + 128 + c, reinterpret_cast<const uint32_t*>(v));
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.acc_empty);
+    }
+    mbar_wait(&S.acc_full, (runs - 1) & 1, abort, g.status);
     // as a dependent of the quantisation (whose row scales may be read below) this
     // grid does not end before that one
     grid_dependency_wait();
   }
   __syncwarp();
-  const int quad = warp & 3;
   const int at = quad * 32 + lane, row = row0 + at;
-  const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16);
   if (ls == 0) {
     if (warp >= 2) {
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < g.N; c += 16) {
         float v[16];
-        tmem_ld16(taddr + c, reinterpret_cast<uint32_t*>(v));
-        tmem_wait_ld();
+        sums16(c, runs > 1, v);
         store8<OUTER>(g, p, v, row, c);
         store8<OUTER>(g, p, v + 8, row, c + 8);
       }
@@ -253,14 +294,13 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
       tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < g.N; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + c, v);
-        tmem_wait_ld();
+        float v[16];
+        sums16(c, runs > 1, v);
         const uint32_t mine = smem_u32(part + rank * cs * 128 + at);
 #pragma unroll
         for (int j = 0; j < 16; ++j)
           mx::st_cluster_f32(mapa_shared(mine + (uint32_t)(((c + j) & (cs - 1)) * 512), (c + j) >> lcs),
-                             __uint_as_float(v[j]));
+                             v[j]);
       }
     }
     cluster_sync();                                // the partial sums have arrived
@@ -296,7 +336,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, g.cols);
   }
 }
 
@@ -309,6 +349,7 @@ static void shape(Args& g, int num_sms) {
   int ls = 0;
   while (ls < 3 && (tiles << (ls + 1)) <= num_sms && (nk >> (ls + 1)) >= 4) ++ls;
   g.log_splits = ls;
+  g.cols = (nk + (1 << ls) - 1) >> ls > kRun ? 256 : 128;
   const int budget = ((tiles << ls) > num_sms ? 110 : 224) * 1024 - 2048;
   g.ns = std::min(kMaxStages, budget / (A_BYTES + g.b_bytes));
 }
