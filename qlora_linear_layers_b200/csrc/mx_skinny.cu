@@ -67,7 +67,6 @@ struct Args {
   int r, N, RP;             // rank; MMA N (a power of two, 16 to 128); padded width
   int log_splits;
   int ns, b_bytes;          // stages and the bytes of B in one
-  int cols;                 // tensor-memory columns: 128, or 256 with several runs
   int wait_first;           // read nothing before the kernel before this one has ended
   int* status;
 };
@@ -135,12 +134,14 @@ __device__ __forceinline__ void store8(const Args& g, const Problem& p, const fl
   if (p.out && col < g.r) *reinterpret_cast<uint4*>(p.out + (int64_t)row * g.r + col) = pack8(v);
 }
 
-// OUTER: both operands MN-major; RT (down): R [L, r] is.
-template <bool OUTER, bool RT>
+// OUTER: both operands MN-major; RT (down): R [L, r] is.  LONG: several runs (in one
+// kernel with the others, T and U of a backward each took 0.5 us more).
+template <bool OUTER, bool RT, bool LONG>
 __global__ void __launch_bounds__(NUM_THREADS, 2)
 k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_b0,
             const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b1,
             const __grid_constant__ Args g) {
+  constexpr uint32_t kCols = LONG ? 256 : 128;     // tensor-memory columns
   extern __shared__ uint8_t smem_raw[];
   grid_launch_dependents();
   Head& S = *smem_align1024<Head>(smem_raw);
@@ -170,7 +171,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
     mbar_fence_init();
   }
   if (warp == 1) {
-    tmem_alloc(&S.tmem_base, g.cols);
+    tmem_alloc(&S.tmem_base, kCols);
     tmem_relinquish();
   }
   if (warp == 0 && lane == 0) {
@@ -182,13 +183,13 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   volatile int* abort = &S.abort;
-  const int runs = (k1 - k0 + kRun - 1) / kRun;
+  const int runs = LONG ? (k1 - k0 + kRun - 1) / kRun : 1;
   const int quad = warp & 3;
   const uint32_t taddr = tmem + ((uint32_t)(quad * 32) << 16);
   // 16 columns of the accumulator, with the runs before it
   auto sums16 = [&](int c, bool more, float* v) {
     tmem_ld16(taddr + c, reinterpret_cast<uint32_t*>(v));
-    if (more) {
+    if (LONG && more) {
       float w[16];
       tmem_ld16(taddr + 128 + c, reinterpret_cast<uint32_t*>(w));
       tmem_wait_ld();
@@ -232,8 +233,8 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
       int s = 0;
       uint32_t ph = 0;
       for (int i = k0; i < k1; ++i) {
-        const int at = (i - k0) & (kRun - 1);      // stage of the run
-        if (at == 0 && i > k0) {
+        const int at = LONG ? (i - k0) & (kRun - 1) : i - k0;      // stage of the run
+        if (LONG && at == 0 && i > k0) {
           mma_commit(&S.acc_full);
           if (!mbar_wait(&S.acc_empty, ((i - k0) / kRun - 1) & 1, abort, g.status)) break;
         }
@@ -254,7 +255,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
       mbar_wait(&S.acc_full, (runs - 1) & 1, abort, g.status);
     }
   } else {
-    for (int j = 0; j + 1 < runs && mbar_wait(&S.acc_full, j & 1, abort, g.status); ++j) {
+    for (int j = 0; LONG && j + 1 < runs && mbar_wait(&S.acc_full, j & 1, abort, g.status); ++j) {
       __syncwarp();
       tc_fence_after();
 #pragma unroll 1
@@ -336,7 +337,7 @@ k_mx_skinny(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ C
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, g.cols);
+    tmem_dealloc(tmem, kCols);
   }
 }
 
@@ -349,16 +350,15 @@ static void shape(Args& g, int num_sms) {
   int ls = 0;
   while (ls < 3 && (tiles << (ls + 1)) <= num_sms && (nk >> (ls + 1)) >= 4) ++ls;
   g.log_splits = ls;
-  g.cols = (nk + (1 << ls) - 1) >> ls > kRun ? 256 : 128;
   const int budget = ((tiles << ls) > num_sms ? 110 : 224) * 1024 - 2048;
   g.ns = std::min(kMaxStages, budget / (A_BYTES + g.b_bytes));
 }
 
-template <bool OUTER, bool RT>
-static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
+template <bool OUTER, bool RT, bool LONG>
+static int launch_kernel(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
                   const Args& g, bool beside, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_devs{0};
-  set_smem_attr_once(k_mx_skinny<OUTER, RT>, 224 * 1024, attr_devs);
+  set_smem_attr_once(k_mx_skinny<OUTER, RT, LONG>, 224 * 1024, attr_devs);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(g.p[0].tiles + g.p[1].tiles) << g.log_splits, 1, 1);
   cfg.blockDim = dim3(NUM_THREADS, 1, 1);
@@ -373,7 +373,15 @@ static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMa
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = beside ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, k_mx_skinny<OUTER, RT>, a0, b0, a1, b1, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, k_mx_skinny<OUTER, RT, LONG>, a0, b0, a1, b1, g) == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+template <bool OUTER, bool RT>
+static int launch(const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& a1, const CUtensorMap& b1,
+                  const Args& g, bool beside, cudaStream_t s) {
+  const int nk = (g.L + 63) / 64;                  // a rank has at most this / 2^log_splits, rounded up
+  return (nk + (1 << g.log_splits) - 1) >> g.log_splits > kRun ? launch_kernel<OUTER, RT, true>(a0, b0, a1, b1, g, beside, s)
+                                                               : launch_kernel<OUTER, RT, false>(a0, b0, a1, b1, g, beside, s);
 }
 
 }  // namespace skinny
