@@ -195,6 +195,21 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launches
+// ---------------------------------------------------------------------------
+// The next grid, if it was launched as a dependent, may start once every CTA of
+// this one has passed here; it waits for this grid's end where it needs it.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Wait for the grid that this one was launched after (returns at once when the
+// launch had no such attribute).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -226,7 +241,9 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
 
 // Bounded wait: returns false (and records QLORA_ERR_TIMEOUT) if the phase
 // does not complete within the wait limit.  `abort` is a CTA-shared flag: once
-// any waiter gives up, the others stop waiting too.
+// any waiter gives up, the others stop waiting too.  AFTER_GRID: the limit counts
+// from the end of the grid that this one was launched after.
+template <bool AFTER_GRID = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
                                           volatile int* abort, int* st) {
   // The clock and the limit (a global load) are read only once the wait has
@@ -236,6 +253,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
     if (mbar_try_wait(bar, parity)) return true;
     if ((i & 255u) == 0) {
       if (*abort) return false;
+      if (AFTER_GRID && t0 == 0) grid_dependency_wait();
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
       else if (now - t0 > wait_limit_ns(st)) break;
@@ -350,21 +368,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* v) {
 }
 
 // ---------------------------------------------------------------------------
-// Programmatic dependent launches
-// ---------------------------------------------------------------------------
-// The next grid, if it was launched as a dependent, may start once every CTA of
-// this one has passed here; it waits for this grid's end where it needs it.
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-
-// Wait for the grid that this one was launched after (returns at once when the
-// launch had no such attribute).
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// ---------------------------------------------------------------------------
 // Thread-block clusters and the paired-SM (cta_group::2) forms
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -401,6 +404,7 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t pa
 }
 
 // Bounded wait on a barrier that the peer CTA also signals.
+template <bool AFTER_GRID = false>
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
                                                   volatile int* abort, int* st) {
   uint64_t t0 = 0;                               // read late, as in mbar_wait
@@ -408,6 +412,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if (mbar_try_wait_cluster(bar, parity)) return true;
     if ((i & 255u) == 0) {
       if (*abort) return false;
+      if (AFTER_GRID && t0 == 0) grid_dependency_wait();
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
       else if (now - t0 > wait_limit_ns(st)) break;

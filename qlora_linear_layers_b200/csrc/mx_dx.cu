@@ -140,6 +140,10 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return PAIR ? mbar_wait_cluster(bar, parity, abort, g.status) : mbar_wait(bar, parity, abort, g.status);
   };
+  // where the wait may begin while the kernel before, which writes sU, still runs
+  auto wait_after_grid = [&](uint64_t* bar, uint32_t parity) {
+    return PAIR ? mbar_wait_cluster<true>(bar, parity, abort, g.status) : mbar_wait<true>(bar, parity, abort, g.status);
+  };
   auto load_tile = [&](void* dst, const CUtensorMap* t, uint64_t* bar, int x, int y) {
     if (PAIR) tma_load_2d_pair(dst, t, mapa_shared(smem_u32(bar), 0), x, y);
     else tma_load_2d(dst, t, bar, x, y);
@@ -178,7 +182,7 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
       int s = 0;
       uint32_t ph = 0;
       for (int i = -na; i < k1 - k0; ++i) {
-        if (!wait(&S.full_b[s], ph)) break;
+        if (!wait_after_grid(&S.full_b[s], ph)) break;
         // the converters never fill the first na slots' first use (na <= 2 < NS)
         if (i >= 0 && !wait(&S.full_a[s], ph ^ (s < na ? 1u : 0u))) break;
         tc_fence_after();
@@ -241,7 +245,7 @@ k_mx_dx(const __grid_constant__ CUtensorMap tm_dy,         // [M, rows of W] bf1
         v[2] = mx_values8<FMT>(cw[d].z, s1, rs[d]);
         v[3] = mx_values8<FMT>(cw[d].w, s1, rs[d]);
         load(i + kGroups * kAhead, d);
-        if (lane == 0) ok = wait(&S.empty[s], ph ^ 1);
+        if (lane == 0) ok = wait_after_grid(&S.empty[s], ph ^ 1);
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (!ok) break;
 #pragma unroll
