@@ -466,11 +466,13 @@ void launch_mx_transpose(const void* A, int r, int K, int RP, void* At, cudaStre
 // 16-byte words of both factors (a lane's words hold the same eight j), through
 // shared memory to eight consecutive columns a lane, one Philox block's mask.
 // Bytes: dX read and written; the generator costs about as much (1111 x 3584: 14
-// us).  dX is rounded to bf16 twice, here and by the product before: kept in fp32
-// between the two it would be twice the bytes.
+// us).  sU may still be written when this grid starts, so plain loads read it after
+// the wait; At is complete before the chain's first dependent launch.  dX is rounded
+// to bf16 twice, here and by the product before: kept in fp32 between the two it
+// would be twice the bytes.
 // ===========================================================================
 __global__ void __launch_bounds__(256, 3)
-k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restrict__ At, int RP, int M, int K,
+k_mx_rank_add(const __nv_bfloat16* sU, const __nv_bfloat16* __restrict__ At, int RP, int M, int K,
               __nv_bfloat16* dX, const __grid_constant__ DropoutKeys keys) {
   __shared__ __align__(16) float s_ad[8][16][36];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -486,7 +488,7 @@ k_mx_rank_add(const __nv_bfloat16* __restrict__ sU, const __nv_bfloat16* __restr
     uint4 a[2], b[4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      a[h] = m0 + 8 * h + g < M ? __ldg(reinterpret_cast<const uint4*>(sU + (int64_t)(m0 + 8 * h + g) * RP + j))
+      a[h] = m0 + 8 * h + g < M ? *reinterpret_cast<const uint4*>(sU + (int64_t)(m0 + 8 * h + g) * RP + j)
                                 : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 4; ++i)                    // K % 32 == 0
