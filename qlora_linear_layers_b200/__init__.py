@@ -249,8 +249,9 @@ def qlora_linear_bwd_dropout(w: NF4Tensor, X, dY, A, B, alpha: float, p: float, 
                "qlora_linear_bwd_dropout")
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice      # without the initialisation that a CUDA tensor implies
+# None where torch was built without CUDA: no tensor gets as far as a call of these there
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)    # without the initialisation that a CUDA tensor implies
 
 
 class _On:
