@@ -289,6 +289,13 @@ def _dense(dev: int, dtype, shape: tuple, t, what: str) -> int | None:
     return t.data_ptr()
 
 
+def _scratch(ws, dev: int) -> tuple:
+    """(address, bytes) of a workspace tensor of any type on this device."""
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: expected a contiguous tensor on CUDA device {dev}, got one on {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def _rows_of(t, what: str) -> int:
     """Row stride in elements of a 2-D CUDA tensor whose rows are contiguous."""
     if t.get_device() < 0 or t.dim() != 2:
@@ -400,7 +407,7 @@ def _mx_fwd(w, X, A, B, alpha, Y, T, save_T, p, seed, ws, stream):
             op = _lib.QLORA_OP_MX_FWD if dr is None else _lib.QLORA_OP_MX_FWD_DROPOUT
             ws = _mx_workspace(op, M, w, r, X)
         _lib.check(_lib.load().qlora_mx_linear_fwd(cw, x, M, a, b, r, alpha, dr, Y.data_ptr(), _ptr(T),
-                                                   ws.data_ptr(), ws.numel(), s),
+                                                   *_scratch(ws, dev), s),
                    "qlora_mx_linear_fwd")
     return Y, T
 
@@ -436,7 +443,7 @@ def _mx_bwd(w, X, dY, A, B, alpha, dX, dA, dB, T, p, seed, ws, stream):
             op = _lib.QLORA_OP_MX_BWD if dr is None else _lib.QLORA_OP_MX_BWD_DROPOUT
             ws = _mx_workspace(op, M, w, r, X)
         _lib.check(_lib.load().qlora_mx_linear_bwd(cw, x, dy, M, a, b, r, alpha, dr, t, dX.data_ptr(),
-                                                   _ptr(dA), _ptr(dB), ws.data_ptr(), ws.numel(), s),
+                                                   _ptr(dA), _ptr(dB), *_scratch(ws, dev), s),
                    "qlora_mx_linear_bwd")
     return dX, dA, dB
 
