@@ -81,3 +81,42 @@ def test_layer_far_row_scales(q, M, N, K):
     assert float(((T.double() - t).abs() - H * t.abs() - (1 + H) * K * U * t_mag - TINY).max()) <= 0
     ad = s * (H * t.abs() + (1 + H) * K * U * t_mag) @ b.abs().T       # T's sum, and s T in bf16
     check(Y, ref, H * ref.abs() + (1 + H) * (ad + (K + r + 3) * U * (mag + (1 + H) * s * t_mag @ b.abs().T)))
+
+
+@pytest.mark.parametrize("fmt", [mx.MXFP4, mx.NVFP4])
+@pytest.mark.parametrize("p", [0.0, 0.25])
+@pytest.mark.parametrize("M,N,K", [(1, 136, 256), (20, 136, 4096), (40, 136, 192), (200, 520, 320), (33, 264, 4096), (600, 264, 128)])
+def test_zero_rows_of_the_weight(q, fmt, p, M, N, K):
+    """Rows of zeros in W, forward and backward: the adapter's term is all of their
+    outputs, and they add nothing but it to dX."""
+    r, s, seed, bf = 16, 2.0, 11, torch.bfloat16
+    g = torch.Generator("cuda").manual_seed(M + K)
+    rn = lambda *k: torch.randn(*k, generator=g, device="cuda")
+    W = rn(N, K)
+    W[8:80] = 0
+    X, A, B, dY = rn(M, K).to(bf), (rn(r, K) * 0.1).to(bf), rn(N, r).to(bf), rn(M, N).to(bf)
+    X[M // 2] = 0
+    w = q.mx_quantize(W, fmt)
+    Y, T = q.mx_linear_fwd(w, X, A, B, s * r, p=p, seed=seed)
+    dX, dA, dB = q.mx_linear_bwd(w, X, dY, A, B, s * r, p=p, seed=seed, T=T)
+    assert q.qlora_check_status() == 0
+    vx, vw = q.mx_dequantize(q.mx_quantize(X, fmt)).double(), q.mx_dequantize(w).double()
+    assert bool((vw[8:80] == 0).all())
+    xd = q.dropout_fwd(X, p, seed).double()
+    keep = (q.dropout_fwd(torch.ones_like(X), p, seed) != 0).double() / (1 - p)
+    a, b, d = A.double(), B.double(), dY.double()
+    t, t_mag = xd @ a.T, xd.abs() @ a.abs().T
+    ref, mag = vx @ vw.T + s * t @ b.T, vx.abs() @ vw.abs().T
+    ad = s * (H * t.abs() + (1 + H) * K * U * t_mag) @ b.abs().T
+    check(Y, ref, H * ref.abs() + (1 + H) * (ad + (K + r + 3) * U * (mag + (1 + H) * s * t_mag @ b.abs().T)))
+    assert bool((Y[M // 2] == 0).all())
+    u, u_mag = d @ b, d.abs() @ b.abs()
+    ue = s * (H * u.abs() + (1 + H) * N * U * u_mag)            # s U: its sum, and its rounding
+    ref, mag = d @ vw + keep * s * (u @ a), d.abs() @ vw.abs()
+    ad = keep * (ue @ a.abs() + (N + r + 4) * U * (1 + H) * s * (u_mag @ a.abs()))
+    twice = H * (d @ vw).abs() if p else 0                      # with dropout dX is rounded twice
+    check(dX, ref, H * ref.abs() + (1 + 2 * H) * (ad + twice + (N + 1) * U * mag))
+    ref = s * u.T @ xd
+    check(dA, ref, H * ref.abs() + (1 + H) * (ue.T @ xd.abs() + M * U * (1 + H) * s * u_mag.T @ xd.abs()))
+    ref = s * d.T @ T.double()
+    check(dB, ref, H * ref.abs() + (1 + H) * (M + 1) * U * s * d.abs().T @ T.double().abs())
