@@ -114,7 +114,9 @@ BwdWs bwd_ws(int64_t M, int64_t N, int64_t K, int r) {
 // Forward workspace of the layer on a microscaled base: the quantised tokens
 // (codes, scale tiles, row scales), then the adapter's factors as the product
 // reads them (sT [M, RP], Bpad [N, RP]) and, with dropout, X' [M, K]; r = 0 has
-// none of these.
+// none of these.  Bpad is reserved although only the product with the adapter as K
+// steps uses it: that choice depends on the device's SM count, this size, which a
+// host without a GPU can ask for, does not.  The same holds for Wt below.
 struct MxFwdWs {
   size_t xq, xs, xr, sT, Bpad, xd, total;
 };
@@ -134,9 +136,9 @@ MxFwdWs mx_fwd_ws(int64_t M, int64_t N, int64_t K, int r, bool dropout) {
   return w;
 }
 
-// Its backward: Wt = deq(W)^T [K, N] where dX does not expand the weight inside,
-// and with an adapter T [M, r] (recomputed when not passed), sU [M, RP], At [K, RP]
-// and, with dropout, X' [M, K] (all bf16).
+// Its backward: Wt = deq(W)^T [K, N] (reserved for any M; written where dX does not
+// expand the weight inside), and with an adapter T [M, r] (recomputed when not
+// passed), sU [M, RP], At [K, RP] and, with dropout, X' [M, K] (all bf16).
 struct MxBwdWs {
   size_t Wt, T, sU, At, xd, total;
 };

@@ -27,7 +27,8 @@ template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
 
-// The general kernel: any width, strides and first number.  One thread a
+// The general kernel, element by element (8192 x 3584 from number 1: 108 us bf16, 142 us
+// fp32, against 45 and 46 us of the one below): any width, strides and first number.  One thread a
 // Philox block: elements 8 blk .. 8 blk + 7 of the numbering that starts at 0,
 // of which [first, first + rows * cols) exist here.
 template <typename T>

@@ -87,8 +87,9 @@ bool mx_adapter_in_epilogue(int M, int N, int K, int num_sms);
 
 // Y[M, N] = deq(x) deq(w)^T + the adapter's term.  after_prep: launched as the
 // dependent of the kernel before it (launch_mx_prep, launch_mx_quantize or
-// launch_mx_down), with whose end x, sT and tok are complete; w and its adapter
-// factor were before that one began.  QLORA_OK or QLORA_ERR_CUDA.
+// launch_mx_down), with whose end x, sT, tok and wt are complete: the kernel that
+// writes wt (launch_mx_pad_rows) may still run when this one starts.  Only w, its
+// scales and B may be read before the wait for that end.  QLORA_OK or QLORA_ERR_CUDA.
 int launch_mx_gemm(const qlora_mx_tensor* x, const qlora_mx_tensor* w, const MxAdapter& ad, bool after_prep, void* Y,
                    int* status, cudaStream_t s, int num_sms);
 

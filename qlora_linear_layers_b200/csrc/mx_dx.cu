@@ -20,11 +20,12 @@
 //    SMs (tcgen05 cta_group::2) with a tile of 256 columns x 256 tokens, each
 //    expanding its own 128 columns and loading half of the tokens.
 //
-// Bound: a stage is 4 (45 + BN / 2) cycles of MMA (692 at 256 tokens), about 400
-// of converter issue, and at 256 tokens 96 KB of shared-memory traffic (750
-// cycles; 64 KB in a pair: W 18944 x 3584, 1111 tokens 140 us against 150, 470 ns a
-// stage at the clock that the tensor cores' power leaves).  Every tile of tokens expands the weight again, so from some token count
-// on the expansion to HBM and the paired-SM GEMM are cheaper (dx_cost).
+// Bound: a stage is 4 (45 + BN / 2) cycles of MMA (692 at 256 tokens; the pipe needs 4
+// BN / 2 of them, see mx_gemm_pair.cu), about 400 of converter issue, and at 256
+// tokens 96 KB of shared-memory traffic (750 cycles; 64 KB in a pair: W 18944 x 3584,
+// 1111 tokens 140 us against 150, 470 ns a stage at the clock that the tensor cores'
+// power leaves).  Every tile of tokens expands the weight again, so from some token
+// count on the expansion to HBM and the paired-SM GEMM are cheaper (cost_expanded).
 // Every wait is bounded (QLORA_ERR_TIMEOUT).
 
 #include <algorithm>

@@ -6,10 +6,12 @@
 //   and PN / 2 of the tokens, so a stage (256 elements of K) brings half the
 //   token codes to each SM.
 //
-// The tensor core is the bound.  Measured on B200, one MMA (256 x PN x 64)
-// takes 45 + PN / 2 cycles whatever its kind and operands, so a tile is as wide
-// as the rounds of tiles allow (up to 256 tokens), and the issuing thread has
-// to keep up with it:
+// The tensor core is the bound.  In this kernel, and in a loop of its MMAs on two
+// stages alone, one MMA (256 x PN x 64) takes 45 + PN / 2 cycles.  The pipe needs
+// PN / 2 of them, and the bf16 kernel of gemm_pair.cu spends 137 on a tile of 224
+// tokens, ramps included, so the 45 are not the hardware's least; what they go to is
+// not known.  They make a tile as wide as the rounds of tiles allow (up to 256
+// tokens), and the issuing thread has to keep up:
 //  * a stage's 3 NT scale copies and 4 MMAs leave one thread in about 570
 //    cycles (NVFP4) against 694 of MMA time; nothing else is in its loop;
 //  * each pipeline stage has scale columns of its own in tensor memory (PN <=
@@ -25,7 +27,8 @@
 //    hide that read too, but with tiles of 192 tokens, whose MMAs do 8 % less per
 //    cycle.
 // 8192 x 18944 x 3584 with r = 64: 211 us MXFP4, 219 us NVFP4 (5.4 and 5.2 PFLOP/s),
-// 97 % of those cycles at the 1.64 GHz that the tensor cores' power leaves.
+// 97 % of those cycles at the 1.64 GHz that the tensor cores' power leaves; the
+// tensor pipe is active in 75 % of them.
 // The adapter's bf16 K steps (kind::f16) come first and are complete before the
 // block-scaled MMAs of the tile begin: MMAs of two kinds need not run in order.
 // With one round of tiles the epilogue adds the adapter instead, on warp-level
@@ -420,7 +423,7 @@ k_mx_gemm_pair(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__
   }
 }
 
-// Tokens of a tile: a round of tiles takes about nk stages of 4 (45 + PN / 2)
+// Tokens of a tile: a round of tiles takes about nk stages of 4 (45 + PN / 2) measured
 // cycles and 1000 for the accumulator's read and the ramp, so the cheapest of
 // 128, 192 and 256 depends on how full it leaves the last round.
 static int pair_tokens(const Args& a, int num_sms, int64_t* cycles) {
