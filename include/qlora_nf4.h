@@ -432,10 +432,12 @@ int qlora_mx_matmul(const qlora_mx_tensor* x, const qlora_mx_tensor* w, void* Y,
  * the layer without an adapter.  The adapter runs in the product's own
  * accumulator, or is added after it, as the sizes decide: in the accumulator,
  * with NVFP4, its bf16 factors s T and B are divided by the row scales of X and
- * of W (exact for powers of two).  It has to be finite so divided: with the scales
- * s_n of W that the quantiser writes it is while s 2688 sum |A| |B| < 2^128 s_n
- * for every row n (2^28 for the smallest scale).  The outputs and ws overlap
- * neither an input nor one another, here and in the backward.
+ * of W (exact for powers of two).  It has to be finite so divided.  With scales as
+ * the quantiser writes them it is while, for every row n of W and its scale s_n,
+ * |B_n| < 2^127 s_n and 2688 s c sum |A| |B_n| < 2^127 s_n, the sum over both
+ * indices of A (2^27 on the right for the smallest scale; c = 1 without dropout).
+ * The outputs and ws overlap neither an input nor one another, here and in the
+ * backward.
  * Constraints: M >= 1, N % 8 == 0, K % 64 == 0, r in {0, 8, 16, 32, 64, 128},
  * ws of qlora_workspace_bytes(QLORA_OP_MX_FWD, M, N, K, r) bytes, with dropout
  * of QLORA_OP_MX_FWD_DROPOUT.
